@@ -10,6 +10,8 @@ Layouts (see include/fp8q.h):
   activation scales  group-major fp32 [K/128, ld]   (scale of row m, group g at [g, m])
   weight scales      fp32 [N/128, K/128]
   E4M3 tensors       torch.uint8 (view as torch.float8_e4m3fn if wanted)
+  INT8 operands      torch.int8 [rows, K] with one fp32 scale per row
+  gated weights      [2N, K]: the gate's N rows, then the up projection's N
 """
 from __future__ import annotations
 
@@ -57,6 +59,13 @@ SIGNATURES = {
     "fp8_gemm_grouped": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32,
                                 _i64, _i64, _i64, _vp]),
     "fp8_gemm_nopromo": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp]),
+    "fp8q_quant_int8_rowwise": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "fp8q_gemm_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp]),
+    "fp8q_gemm_int8_gated": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp]),
+    "fp8_gemm_blockscaled_gated": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
+                                          _i64, _i64, _i64, _vp]),
+    "fp8q_gated_backward_quant": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                         _i64, _vp, _i64, _i32, _vp]),
     "fp8q_get_device_error": (_i32, [_vp]),
     "fp8q_selftest_wait_timeout": (_i32, [ctypes.c_uint64, _vp]),
     "fp8q_status_string": (ctypes.c_char_p, [_i32]),
@@ -482,6 +491,167 @@ def gemm_nopromo(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch
         _call("fp8_gemm_nopromo", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
               out.data_ptr(), M, N, K, qa.stride(0), qb.stride(0), out.stride(0), _stream(qa))
     return out
+
+
+# --------------------------------------------------------------------------------------
+# 8-bit feed-forward: INT8 products and the gated projections
+# --------------------------------------------------------------------------------------
+
+def _ceil_to(n: int, multiple: int) -> int:
+    return -(-n // multiple) * multiple
+
+
+def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """One scale per row: x bf16 [M, K] -> (q int8 [M, K], s fp32 [M]), x ~ q s.
+
+    Per token for activations, per output channel for weights.  Any K; the codes' rows are
+    allocated 16 bytes apart or a multiple (q is a view of such a buffer when K % 16 != 0),
+    as the products need them.  A row that holds Inf or NaN gets the scale NaN.
+    """
+    _need(x, torch.bfloat16, "x", 2)
+    M, K = x.shape
+    if K == 0:
+        raise ValueError("x must have at least one column")
+    if out is None:
+        q = torch.empty((M, _ceil_to(K, 16)), dtype=torch.int8, device=x.device)[:, :K]
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    else:
+        q, s = out
+        _rows(q, torch.int8, "q", M, K, x.device)
+        _vector(s, "s", M, x.device)
+    with _on(x):
+        _call("fp8q_quant_int8_rowwise", x.data_ptr(), M, K, x.stride(0), q.data_ptr(), q.stride(0),
+              s.data_ptr(), _stream(x))
+    return q, s
+
+
+def _vector(t: torch.Tensor, name: str, n: int, device: torch.device) -> None:
+    """A 1-D fp32 operand of at least n contiguous elements on `device`."""
+    _need(t, torch.float32, name, 1)
+    _same_device(t, device, name)
+    if t.shape[0] < n:
+        raise ValueError(f"{name} must hold at least {n} scales, got {t.shape[0]}")
+
+
+def _int8_operands(qa, sa, qb, sb):
+    """Checks of the INT8 products' operands; returns (M, rows of qb, K)."""
+    _need(qa, torch.int8, "qa", 2)
+    _need(qb, torch.int8, "qb", 2)
+    M, K = qa.shape
+    rows = qb.shape[0]
+    if qb.shape[1] != K:
+        raise ValueError("qa and qb disagree on K")
+    _same_device(qb, qa.device, "qb")
+    _vector(sa, "sa", M, qa.device)
+    _vector(sb, "sb", rows, qa.device)
+    return M, rows, K
+
+
+def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor,
+              out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C[m, n] = (sum_k qa[m, k] qb[n, k]) sa[m] sb[n], the sum exact.
+
+    qa int8 [M, K], sa fp32 [M] (per token); qb int8 [N, K], sb fp32 [N] (per channel); C bf16
+    or fp32 [M, N].  Any M, N and K <= 131071; the rows of qa and qb start on 16 bytes
+    (quant_int8_rowwise lays them out so).
+    """
+    M, N, K = _int8_operands(qa, sa, qb, sb)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+    else:
+        _rows(out, out.dtype, "out", M, N, qa.device)
+    code = _out_code(out.dtype)
+    with _on(qa):
+        _call("fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
+              out.data_ptr(), code, M, N, K, qa.stride(0), qb.stride(0), out.stride(0), _stream(qa))
+    return out
+
+
+def gemm_int8_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h = silu(g) u with g, u the INT8 products of qa with the gate's and the up projection's rows.
+
+    qa int8 [M, K], sa fp32 [M]; qw int8 [2N, K] (gate rows, then up rows), sw fp32 [2N];
+    h bf16 [M, N].  Sizes and alignment as ``gemm_int8``.
+    """
+    M, rows, K = _int8_operands(qa, sa, qw, sw)
+    if rows % 2:
+        raise ValueError("qw must have an even number of rows: the gate's, then the up projection's")
+    N = rows // 2
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
+    else:
+        _rows(out, torch.bfloat16, "out", M, N, qa.device)
+    with _on(qa):
+        _call("fp8q_gemm_int8_gated", qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(),
+              out.data_ptr(), M, N, K, qa.stride(0), qw.stride(0), out.stride(0), _stream(qa))
+    return out
+
+
+def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+                           with_gu: bool = False, out=None):
+    """h = silu(g) u with g, u the block-scaled FP8 products of qa with the gate's and the up
+    projection's rows, in one kernel.
+
+    qa uint8 [M, K], sa fp32 [K/128, >= M]; qw uint8 [2N, K] (gate rows, then up rows),
+    sw fp32 [2N/128, K/128]; h bf16 [M, N].  ``with_gu``: returns (h, gu) with gu bf16 [M, 2N]
+    (g, then u) kept for ``gated_backward_quant``.  ``out``: h, or (h, gu) with ``with_gu``, to
+    write into.  Any M; N and K multiples of 128; FP32 or power-of-two scales.
+    """
+    qa, qw = _u8(qa), _u8(qw)
+    h, gu = (out if with_gu else (out, None)) if out is not None else (None, None)
+    qa, qw, _, M, rows, K = _dense_gemm_operands(qa, sa, qw, sw, False, None, torch.bfloat16, alloc=False)
+    if rows % 256:
+        raise ValueError("qw must have 2N rows with N a multiple of 128")
+    N = rows // 2
+    if out is None:
+        h = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
+        gu = torch.empty((M, rows), dtype=torch.bfloat16, device=qa.device) if with_gu else None
+    else:
+        _rows(h, torch.bfloat16, "h", M, N, qa.device)
+        if with_gu:
+            _rows(gu, torch.bfloat16, "gu", M, rows, qa.device)
+    with _on(qa):
+        _call("fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), sa.stride(0), qw.data_ptr(),
+              sw.data_ptr(), h.data_ptr(), h.stride(0), gu.data_ptr() if with_gu else None,
+              gu.stride(0) if with_gu else 0, M, N, K, qa.stride(0), qw.stride(0), _stream(qa))
+    return (h, gu) if with_gu else h
+
+
+def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False, out=None):
+    """Gradient of silu(g) u with respect to g and u, quantized for the two gradient products.
+
+    dh bf16 [M, N], gu bf16 [M, 2N] -> (q uint8 [M, 2N], s fp32 [2N/128, M], qt uint8 [2N, Mp],
+    st fp32 [Mp/128, 2N]), Mp = M rounded up to 128: the 1x128 quantizations of D = [dg | du]
+    (bf16, never written) and of its transpose, whose columns past M are zero.  N % 128 == 0.
+    """
+    _need(dh, torch.bfloat16, "dh", 2)
+    _need(gu, torch.bfloat16, "gu", 2)
+    M, N = dh.shape
+    dev = dh.device
+    _same_device(gu, dev, "gu")
+    if tuple(gu.shape) != (M, 2 * N):
+        raise ValueError(f"gu must be [{M}, {2 * N}], got {tuple(gu.shape)}")
+    if N % 128:
+        raise ValueError("dh must have a multiple of 128 columns")
+    Mp = _ceil_to(M, 128)
+    if out is None:
+        q = torch.empty((M, 2 * N), dtype=torch.uint8, device=dev)
+        s = torch.empty((2 * N // 128, M), dtype=torch.float32, device=dev)
+        qt = torch.empty((2 * N, Mp), dtype=torch.uint8, device=dev)
+        st = torch.empty((Mp // 128, 2 * N), dtype=torch.float32, device=dev)
+    else:
+        q, s, qt, st = out
+        _rows(_u8(q), torch.uint8, "q", M, 2 * N, dev)
+        _rows(s, torch.float32, "s", 2 * N // 128, M, dev)
+        _rows(_u8(qt), torch.uint8, "qt", 2 * N, Mp, dev)
+        _rows(st, torch.float32, "st", Mp // 128, 2 * N, dev)
+    q8, qt8 = _u8(q), _u8(qt)
+    with _on(dh):
+        _call("fp8q_gated_backward_quant", dh.data_ptr(), dh.stride(0), gu.data_ptr(), gu.stride(0), M, N,
+              q8.data_ptr(), q8.stride(0), s.data_ptr(), s.stride(0), qt8.data_ptr(), qt8.stride(0),
+              st.data_ptr(), st.stride(0), int(bool(pow2)), _stream(dh))
+    return q, s, qt, st
 
 
 def device_error(device=None) -> int:

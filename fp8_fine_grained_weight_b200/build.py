@@ -15,14 +15,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8q.so")
-SOURCES = [os.path.join(CSRC, "fp8q.cu")]
+SOURCES = [os.path.join(CSRC, "library.cu")]    # one translation unit: it includes the other .cu files
 
 
 def deps() -> list:
-    """Every file the library is built from: the sources, every header under csrc/ and the
+    """Every file the library is built from: the sources and headers under csrc/ and the
     public header.  A change to any of them makes the next build() recompile."""
-    hdrs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
-    return SOURCES + hdrs + [os.path.join(ROOT, "include", "fp8q.h")]
+    files = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h")))
+    return files + [os.path.join(ROOT, "include", "fp8q.h")]
 
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -1,0 +1,217 @@
+// Entry points of the 8-bit feed-forward operators declared in include/fp8q.h: per-row INT8
+// quantization, INT8 products, and the gated projections with their backward pass.  Part of
+// library.cu's translation unit (after fp8q.cu, whose host helpers it uses).
+#include "gated.cuh"
+#include "int8.cuh"
+
+namespace {
+
+using fp8q::GatedArgs;
+using fp8q::GatedBwdArgs;
+using fp8q::Int8Args;
+
+// CTAs of `kern` that fit the current device at once; sets its shared memory limit on first
+// use.  0 on failure.
+template <auto kern>
+int resident_ctas(int threads, uint32_t smem) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev].load(std::memory_order_acquire);
+  if (n) return n;
+  int sms = 0, per_sm = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+          cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm <= 0) {
+    (void)cudaGetLastError();   // handled here, not by the next launch check
+    return 0;
+  }
+  n = sms * per_sm;
+  cached[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
+
+constexpr int64_t kInt8MaxK = 131071;   // K 128^2 <= 2^31 - 1: the INT32 sums are exact
+
+int check_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, const void* C, int out_dtype,
+               int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc) {
+  if (M < 0 || N < 0 || K < 0) return FP8Q_ERR_SHAPE;
+  if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_FP32) return FP8Q_ERR_UNSUPPORTED;
+  if (!A || !sA || !B || !sB || !C) return FP8Q_ERR_NULL;
+  if (N == 0 || K == 0 || K > kInt8MaxK || M > 0x3FFFFFFF || N > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  if (lda < K || ldb < K || ldc < N) return FP8Q_ERR_SHAPE;
+  if (lda % 16 != 0 || ldb % 16 != 0 || !aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 4) || !aligned(sB, 4) ||
+      !aligned(C, out_dtype == FP8Q_OUT_BF16 ? 2 : 4))
+    return FP8Q_ERR_ALIGN;
+  return FP8Q_OK;
+}
+
+// Columns of B per tile: the width with the least time over all waves.  A tile's time per
+// K step is the larger of its products (width / 2 cycles at 8192 products a cycle) and its
+// operands' way out of shared memory ((128 + width) / 4 cycles at 128 bytes a cycle).
+int int8_width(int64_t M, int64_t rows, bool gated, int units) {
+  const int step = gated ? 64 : 32;
+  const int64_t mt = (M + 127) / 128;
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int w = 256; w >= step; w -= step) {
+    const int64_t waves = (mt * ((rows + w - 1) / w) + units - 1) / units;
+    const int64_t cost = waves * (2 * w > 128 + w ? 2 * w : 128 + w);
+    if (cost < best_cost) best = w, best_cost = cost;
+  }
+  return best;
+}
+
+template <bool GATED, bool OUT_BF16>
+int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M, int64_t N,
+             int64_t K, int64_t lda, int64_t ldb, int64_t ldc, void* stream) {
+  using Cfg = fp8q::Int8Cfg;
+  static constexpr auto kern = fp8q::gemm_int8_kernel<GATED, OUT_BF16>;
+  const int units = resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes);
+  if (units <= 0) return FP8Q_ERR_CUDA;
+  const int64_t rows = GATED ? 2 * N : N;
+  Int8Args a{};
+  a.sA = sA; a.sB = sB; a.C = C; a.ldc = ldc; a.M = M; a.N = N;
+  a.k_groups = static_cast<int>((K + 127) / 128);
+  a.width = int8_width(M, rows, GATED, units);
+  const int cols = GATED ? a.width / 2 : a.width;
+  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + cols - 1) / cols;
+  if (mt * nt > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  a.mt = static_cast<int>(mt);
+  a.nt = static_cast<int>(nt);
+  a.n_fastest = M > rows;
+  a.vec = (ldc * (OUT_BF16 ? 2 : 4)) % 16 == 0 && aligned(C, 16);
+  CUtensorMap tmA, tmB;
+  int st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM);
+  if (st != FP8Q_OK || (st = encode_operand(&tmB, B, K, rows, ldb, cols)) != FP8Q_OK) return st;
+  const int64_t grid = mt * nt < units ? mt * nt : units;
+  kern<<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::smem_bytes, static_cast<cudaStream_t>(stream)>>>(tmA, tmB, a);
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8q_quant_int8_rowwise(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* q, int64_t ldq, float* scales,
+                            void* stream) {
+  if (M < 0 || K < 0) return FP8Q_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8Q_OK;
+  if (!x || !q || !scales) return FP8Q_ERR_NULL;
+  if (ldx < K || ldq < K || M > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  if (!aligned(x, 2) || !aligned(scales, 4)) return FP8Q_ERR_ALIGN;
+  const auto* xs = static_cast<const uint16_t*>(x);
+  const auto st = static_cast<cudaStream_t>(stream);
+  constexpr int T = fp8q::kInt8Threads, V = 8 * fp8q::kInt8Vecs;
+  const auto m32 = static_cast<unsigned>(M);
+  if (K % 8 != 0 || ldx % 8 != 0 || !aligned(x, 16) || ldq % 8 != 0 || !aligned(q, 8))
+    fp8q::quant_int8_any_kernel<<<m32, T, 0, st>>>(xs, K, ldx, q, ldq, scales);
+  else if (K <= 32 * V)
+    fp8q::quant_int8_rows_kernel<32, true><<<m32 / 8 + (m32 % 8 != 0), T, 0, st>>>(xs, M, K, ldx, q, ldq, scales);
+  else if (K <= T * V)
+    fp8q::quant_int8_rows_kernel<T, true><<<m32, T, 0, st>>>(xs, M, K, ldx, q, ldq, scales);
+  else
+    fp8q::quant_int8_rows_kernel<T, false><<<m32, T, 0, st>>>(xs, M, K, ldx, q, ldq, scales);
+  return launched();
+}
+
+int fp8q_gemm_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int out_dtype,
+                   int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, void* stream) {
+  if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
+  const int st = check_int8(A, sA, B, sB, C, out_dtype, M, N, K, lda, ldb, ldc);
+  if (st != FP8Q_OK) return st;
+  return out_dtype == FP8Q_OUT_BF16 ? run_int8<false, true>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, stream)
+                                    : run_int8<false, false>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, stream);
+}
+
+int fp8q_gemm_int8_gated(const int8_t* A, const float* sA, const int8_t* W, const float* sW, void* H, int64_t M,
+                         int64_t N, int64_t K, int64_t lda, int64_t ldw, int64_t ldh, void* stream) {
+  if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
+  const int st = check_int8(A, sA, W, sW, H, FP8Q_OUT_BF16, M, N, K, lda, ldw, ldh);
+  if (st != FP8Q_OK) return st;
+  return run_int8<true, true>(A, sA, W, sW, H, M, N, K, lda, ldw, ldh, stream);
+}
+
+int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W, const float* sW,
+                               void* H, int64_t ldh, void* GU, int64_t ldgu, int64_t M, int64_t N, int64_t K,
+                               int64_t lda, int64_t ldw, void* stream) {
+  using Cfg = fp8q::GatedCfg;
+  if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
+  if (N > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  int st = check_dense_blockscaled(A, sA, ld_sa, W, sW, 0, FP8Q_BSCALE_BLOCK128x128, H, FP8Q_OUT_BF16, M, N, K, lda,
+                                   ldw, ldh);
+  if (st != FP8Q_OK) return st;
+  if (GU != nullptr) {
+    if (ldgu < 2 * N) return FP8Q_ERR_SHAPE;
+    if (ldgu % 8 != 0 || !aligned(GU, 16)) return FP8Q_ERR_ALIGN;
+  }
+  GatedArgs a{};
+  a.sA = sA; a.ld_sa = ld_sa; a.sW = sW;
+  a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = N / Cfg::kTileN;
+  if (mt * nt > 0x7FFFFFFF || mt * nt / 148 * a.G > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  a.mt = static_cast<int>(mt);
+  a.nt = static_cast<int>(nt);
+  a.n_fastest = M > 2 * N;
+  CUtensorMap tmA, tmW, tmH;
+  if ((st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM)) != FP8Q_OK ||
+      (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kBox)) != FP8Q_OK ||
+      (st = encode_output_bf16(&tmH, H, N, M, ldh)) != FP8Q_OK)
+    return st;
+  const auto s = static_cast<cudaStream_t>(stream);
+  static constexpr auto plain = fp8q::gemm_fp8_gated_kernel<false>, keep = fp8q::gemm_fp8_gated_kernel<true>;
+  const int units = GU != nullptr ? resident_ctas<keep>(fp8q::kGemmThreads, Cfg::smem_bytes)
+                                  : resident_ctas<plain>(fp8q::kGemmThreads, Cfg::smem_bytes);
+  if (units <= 0) return FP8Q_ERR_CUDA;
+  const auto grid = static_cast<unsigned>(mt * nt < units ? mt * nt : units);
+  if (GU != nullptr)
+    keep<<<grid, fp8q::kGemmThreads, Cfg::smem_bytes, s>>>(tmA, tmW, tmH, a);
+  else
+    plain<<<grid, fp8q::kGemmThreads, Cfg::smem_bytes, s>>>(tmA, tmW, tmH, a);
+  return launched();
+}
+
+int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int64_t ldgu, int64_t M, int64_t N,
+                              uint8_t* q, int64_t ldq, float* s, int64_t ld_s, uint8_t* qt, int64_t ldqt, float* st,
+                              int64_t ld_st, int pow2_scale, void* stream) {
+  if (M < 0 || N < 0) return FP8Q_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8Q_OK;
+  if (!dH || !GU || !q || !s || !qt || !st) return FP8Q_ERR_NULL;
+  if (N % 128 != 0 || N > 0x3FFFFFFF || M > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  const int64_t mt = (M + 127) / 128;
+  if (lddh < N || ldgu < 2 * N || ldq < 2 * N || ld_s < M || ldqt < 128 * mt || ld_st < 2 * N) return FP8Q_ERR_SHAPE;
+  if (lddh % 8 != 0 || ldgu % 8 != 0 || ldq % 8 != 0 || ldqt % 16 != 0 || !aligned(dH, 16) || !aligned(GU, 16) ||
+      !aligned(q, 8) || !aligned(qt, 16) || !aligned(s, 4) || !aligned(st, 4))
+    return FP8Q_ERR_ALIGN;
+  if (mt > 0x7FFFFFFF / (N / 128)) return FP8Q_ERR_SHAPE;     // one-dimensional grid
+  CUtensorMap tmDh, tmGu;
+  auto enc = tensor_map_encoder();
+  if (!enc || !bind_current_context()) return FP8Q_ERR_CUDA;
+  auto encode = [&](CUtensorMap* tm, const void* base, int64_t cols, int64_t ld) {
+    // bf16 tiles of 128 rows x 64 columns, 128-byte swizzle
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    cuuint32_t box[2] = {64, 128};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!encode(&tmDh, dH, N, lddh) || !encode(&tmGu, GU, 2 * N, ldgu)) return FP8Q_ERR_CUDA;
+  GatedBwdArgs a{q, s, qt, st, ldq, ld_s, ldqt, ld_st, M, N};
+  const auto grid = static_cast<unsigned>(mt * (N / 128));
+  const auto stm = static_cast<cudaStream_t>(stream);
+  static constexpr auto k1 = fp8q::gated_backward_quant_kernel<true>, k0 = fp8q::gated_backward_quant_kernel<false>;
+  if ((pow2_scale ? resident_ctas<k1>(256, fp8q::kGatedBwdSmem) : resident_ctas<k0>(256, fp8q::kGatedBwdSmem)) <= 0)
+    return FP8Q_ERR_CUDA;
+  if (pow2_scale)
+    k1<<<grid, 256, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
+  else
+    k0<<<grid, 256, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
+  return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,418 @@
+// The gated feed-forward projections in block-scaled FP8: both products, the activation and
+// the product of the two in one kernel, and the backward pass's elementwise part fused with
+// the quantization of its result (sm_100a: tcgen05 + TMEM + TMA).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include "ptx.cuh"
+#include "quant.cuh"
+#include "gemm.cuh"
+#include "int8.cuh"
+
+namespace fp8q {
+
+// ---------------------------------------------------------------- forward
+//
+//   g[m, n] = sum_G  P_G sA[m, G] sW[n / 128, G],        P_G over the gate's row n of W
+//   u[m, n] = the same over row N + n of W
+//   h[m, n] = silu(g) u,  silu(g) = g / (1 + exp(-g))
+//
+// W is [2N, K]: the gate's N rows, then the up projection's.  The promotion per 128 K-elements
+// is that of the block-scaled GEMM: partial sums leave TMEM after each group, are multiplied
+// by the group's scales and added in FP32 registers.  g and u stay in FP32 up to h; when the
+// backward pass will need them (GU) they are also stored, rounded to bf16.
+//
+// A tile is 128 rows by 128 columns of h: 256 rows of W.  They are loaded as four boxes of
+// 64 rows (gate 0-63, up 0-63, gate 64-127, up 64-127), so that the 128 accumulator columns
+// of each epilogue warpgroup are 64 gate columns and the same 64 up columns, and each thread
+// holds both factors of its 64 outputs: nothing is exchanged.  Otherwise the roles are the
+// block-scaled GEMM's: warp 0 TMA producer (3 stages of 48 KB; the fourth's room stages
+// h), warp 1 MMA issuer (one commit per group, two alternating accumulators), warp 2 scale
+// producer (slots of four groups), warps 4-11 promotion and epilogue with the register
+// split 40 / 232 (128 * 40 + 256 * 232 <= 384 * 168).
+struct GatedArgs {
+  const float* sA;      // group-major [G][ld_sa]
+  int64_t ld_sa;
+  const float* sW;      // [2N / 128][G]
+  __nv_bfloat16* gu;    // [M, 2N] when GU
+  int64_t ld_gu, M, N;
+  int G;
+  int mt, nt, n_fastest;
+};
+
+struct GatedCfg {
+  static constexpr int kTileM = 128, kTileN = 128, kN = 256, kStages = 3, kAccBufs = 2;
+  static constexpr int kBox = 64;                       // W rows per TMA box
+  static constexpr uint32_t kABytes = 128 * kBK, kBBytes = kN * kBK, kStageTx = kABytes + kBBytes;
+  static constexpr int kSlotGroups = 4, kScaleSlots = 6;
+  static constexpr uint32_t kGroupFloats = 128 + 4;     // A's row scales, gate and up scale
+  static constexpr uint32_t kSlotFloats = kSlotGroups * kGroupFloats;
+  static constexpr uint32_t kOutWarpBytes = 32 * 64 * 2;   // a warp's 32 x 64 bf16 of h
+  static constexpr uint32_t a = 0;
+  static constexpr uint32_t b = a + kStages * kABytes;
+  static constexpr uint32_t out = b + kStages * kBBytes;
+  static constexpr uint32_t sring = out + kEpiWarps * kOutWarpBytes;
+  static constexpr uint32_t bars = sring + 4 * kScaleSlots * kSlotFloats;
+  // full[S], empty[S], tempty[2], drain, sfull[R], sempty[R]
+  static constexpr uint32_t misc = align_up(bars + 8 * (2 * kStages + kAccBufs + 1 + 2 * kScaleSlots), 16);
+  static constexpr uint32_t smem_bytes = misc + 16 + 1024;
+  static_assert(out % 1024 == 0 && kOutWarpBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kStages >= kAccBufs, "a stage barrier's phase outlives the epilogue's wait for it");
+  static_assert(smem_bytes <= 232448, "fits the 227 KB opt-in shared memory");
+};
+
+// Two FP32 pairs of a column run, rounded to bf16, as 16 bytes.
+__device__ __forceinline__ uint4 bf16x8(const float2& a, const float2& b, const float2& c, const float2& d) {
+  __nv_bfloat162 h0 = __float22bfloat162_rn(a), h1 = __float22bfloat162_rn(b);
+  __nv_bfloat162 h2 = __float22bfloat162_rn(c), h3 = __float22bfloat162_rn(d);
+  return make_uint4(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1),
+                    *reinterpret_cast<uint32_t*>(&h2), *reinterpret_cast<uint32_t*>(&h3));
+}
+
+template <bool GU>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_fp8_gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                          const __grid_constant__ CUtensorMap tmH, const GatedArgs p) {
+  using Cfg = GatedCfg;
+  constexpr int S = Cfg::kStages, NB = Cfg::kAccBufs, R = Cfg::kScaleSlots;
+  constexpr uint32_t SG = Cfg::kSlotGroups;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + Cfg::bars;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + NB);
+  auto sfull_bar = [&](int r) { return bar0 + 8u * (2 * S + NB + 1 + r); };
+  auto sempty_bar = [&](int r) { return bar0 + 8u * (2 * S + NB + 1 + R + r); };
+  float* sring = reinterpret_cast<float*>(smem + Cfg::sring);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::misc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.G;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < NB; ++b) mbar_init(tempty_bar(b), 32 * kEpiWarps);
+    mbar_init(drain_bar, 1);
+    for (int r = 0; r < R; ++r) {
+      mbar_init(sfull_bar(r), 32);                 // one cp.async arrival per producer lane
+      mbar_init(sempty_bar(r), 32 * kEpiWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int tiles = p.mt * p.nt;
+  const int n_tiles = (tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  auto tile_at = [&](int i, int64_t& row0, int64_t& col0) {
+    const int t = blockIdx.x + i * gridDim.x;
+    const int fast = p.n_fastest ? p.nt : p.mt;
+    const int q = t / fast, r = t - q * fast;
+    row0 = static_cast<int64_t>(p.n_fastest ? q : r) * Cfg::kTileM;
+    col0 = static_cast<int64_t>(p.n_fastest ? r : q) * Cfg::kTileN;
+  };
+
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          int64_t row0, col0;
+          tile_at(i, row0, col0);
+          const int32_t gate = static_cast<int32_t>(col0), up = static_cast<int32_t>(p.N + col0);
+          for (int g = 0; g < G; ++g, ++it) {
+            const int s = it % S;
+            if (!mbar_wait(empty_bar(s), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) { ok = false; break; }
+            mbar_arrive_expect_tx(full_bar(s), Cfg::kStageTx);
+            const uint32_t b = sbase + Cfg::b + s * Cfg::kBBytes;
+            tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), g * kBK, static_cast<int32_t>(row0));
+            tma_load_2d(b, &tmW, full_bar(s), g * kBK, gate);
+            tma_load_2d(b + 64 * kBK, &tmW, full_bar(s), g * kBK, up);
+            tma_load_2d(b + 128 * kBK, &tmW, full_bar(s), g * kBK, gate + 64);
+            tma_load_2d(b + 192 * kBK, &tmW, full_bar(s), g * kBK, up + 64);
+          }
+        }
+        const uint32_t first = it > static_cast<uint32_t>(S) ? it - S : 0;
+        for (uint32_t j = first; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, Cfg::kN);
+        const uint32_t total = static_cast<uint32_t>(n_tiles) * G;
+        for (uint32_t it = 0; it < total; ++it) {
+          const int s = it % S;
+          const uint32_t buf = it % NB;
+          // the operands first (long in place), then the accumulator, which comes free just
+          // in time
+          if (!mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) break;
+          if (!mbar_wait(tempty_bar(buf), ((it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t a_addr = sbase + Cfg::a + s * Cfg::kABytes;
+          const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            mma_f8<1>(tmem_base + buf * Cfg::kN, smem_desc_k_sw128(a_addr + 32 * kk),
+                      smem_desc_k_sw128(b_addr + 32 * kk), idesc, kk > 0);
+          mma_commit<1>(empty_bar(s));             // frees the stage and publishes the partial
+        }
+        mma_commit<1>(drain_bar);
+        mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- scale producer
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        int64_t row0, col0;
+        tile_at(i, row0, col0);
+        const float* sW_tile = p.sW + (col0 + (lane & 1) * p.N) / 128 * G;   // lane 0 gate, 1 up
+        for (int g = 0; g < G; ++g, ++it) {
+          const uint32_t sl = it / SG;
+          const int r = sl % R;
+          if (it % SG == 0 && !mbar_wait(sempty_bar(r), ((sl / R) & 1u) ^ 1u, kSiteScales, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = sbase + Cfg::sring + 4u * (Cfg::kSlotFloats * r + Cfg::kGroupFloats * (it % SG));
+          const float* sa_g = p.sA + static_cast<int64_t>(g) * p.ld_sa;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t m = row0 + 32 * j + lane;
+            cp_async_4(slot + 4u * (32 * j + lane), sa_g + (m < p.M ? m : 0), m < p.M);
+          }
+          if (lane < 2) cp_async_4(slot + 4u * (128 + lane), sW_tile + g, true);
+          if (it % SG == SG - 1) cp_async_arrive(sfull_bar(r));
+        }
+      }
+      if (ok && it % SG != 0) cp_async_arrive(sfull_bar((it / SG) % R));   // the last, partial slot
+      cp_async_wait_all();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    // ------------------------------------------------------------ promotion + epilogue
+    const int ew = warp - kEpiWarp0;
+    const int quad = warp & 3, set = ew >> 2;
+    uint32_t acc_it = 0;
+    bool ok = true;
+    uint32_t rbuf[64];
+    float sa4[4] = {0.f, 0.f, 0.f, 0.f}, sg4[4] = {0.f, 0.f, 0.f, 0.f}, su4[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < n_tiles; ++i) {
+      float2 ag[32], au[32];                    // columns 2j, 2j + 1 of the gate's and up's 64
+#pragma unroll
+      for (int j = 0; j < 32; ++j) ag[j] = au[j] = make_float2(0.0f, 0.0f);
+      for (int g = 0; g < G; ++g, ++acc_it) {
+        const uint32_t sl = acc_it / SG;
+        const int r = sl % R;
+        if (acc_it % SG == 0) {                 // a slot's four groups go to registers at once
+          if (ok) ok = mbar_wait(sfull_bar(r), (sl / R) & 1u, kSiteScales, abort_flag);
+          const int base = Cfg::kSlotFloats * r;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sa4[j] = sring[base + Cfg::kGroupFloats * j + quad * 32 + lane];
+            sg4[j] = sring[base + Cfg::kGroupFloats * j + 128];
+            su4[j] = sring[base + Cfg::kGroupFloats * j + 129];
+          }
+          mbar_arrive(sempty_bar(r));
+        }
+        const float2 cg = make_float2(sa4[0] * sg4[0], sa4[0] * sg4[0]);
+        const float2 cu = make_float2(sa4[0] * su4[0], sa4[0] * su4[0]);
+        sa4[0] = sa4[1]; sa4[1] = sa4[2]; sa4[2] = sa4[3];
+        sg4[0] = sg4[1]; sg4[1] = sg4[2]; sg4[2] = sg4[3];
+        su4[0] = su4[1]; su4[1] = su4[2]; su4[2] = su4[3];
+        const uint32_t buf = acc_it % NB;
+        if (ok) ok = mbar_wait(empty_bar(acc_it % S), (acc_it / S) & 1u, kSiteEpilogue, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);       // warp-uniform: TMEM loads are per warp
+        if (ok) {
+          tc_fence_after();
+          const uint32_t taddr =
+              tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * Cfg::kN + set * 128;
+          tmem_ld_64cols(taddr, rbuf);
+          tmem_ld_wait_regs(rbuf);
+          promote_chunk<false>(ag, rbuf, cg, cg, nullptr);
+          promote_chunk<false>(ag + 16, rbuf + 32, cg, cg, nullptr);
+          tmem_ld_64cols(taddr + 64, rbuf);
+          tmem_ld_wait_regs(rbuf);
+          tc_fence_before();
+          mbar_arrive(tempty_bar(buf));         // free for group g + 2
+          promote_chunk<false>(au, rbuf, cu, cu, nullptr);
+          promote_chunk<false>(au + 16, rbuf + 32, cu, cu, nullptr);
+        }
+      }
+      int64_t row0, col0;
+      tile_at(i, row0, col0);
+      const int64_t m0 = row0 + 32 * quad, n0 = col0 + 64 * set;
+      if (!ok || m0 >= p.M) continue;           // warp-uniform
+      if constexpr (GU) {
+        const bool row_ok = m0 + lane < p.M;
+        uint8_t* grow = reinterpret_cast<uint8_t*>(p.gu + (m0 + lane) * p.ld_gu + n0);
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = bf16x8(ag[4 * j], ag[4 * j + 1], ag[4 * j + 2], ag[4 * j + 3]);
+        store_rows_by_quads(v, grow, row_ok);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = bf16x8(au[4 * j], au[4 * j + 1], au[4 * j + 2], au[4 * j + 3]);
+        store_rows_by_quads(v, grow + 2 * p.N, row_ok);
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        ag[j].x = silu_mul(ag[j].x, au[j].x);
+        ag[j].y = silu_mul(ag[j].y, au[j].y);
+      }
+      // h leaves through this warp's 4 KB and one TMA store (which drops rows past M): rows of
+      // 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)
+      const uint32_t stg = sbase + Cfg::out + ew * Cfg::kOutWarpBytes;
+      if (lane == 0) bulk_wait_read_all();      // the previous tile's store has read it
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4),
+                     bf16x8(ag[4 * j], ag[4 * j + 1], ag[4 * j + 2], ag[4 * j + 3]));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&tmH, stg, static_cast<int32_t>(n0), static_cast<int32_t>(m0));
+        bulk_commit_group();
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  if (warp >= kEpiWarp0 && lane == 0) bulk_wait_all();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<1>(tmem_base, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// From dh [M, N] and the stored g, u (bf16 [M, 2N]):
+//
+//   sg = 1 / (1 + exp(-g))
+//   dg = dh u sg (1 + g (1 - sg)),   du = dh g sg          (FP32, rounded to bf16)
+//
+// and of D = [dg | du] [M, 2N] both quantizations the two gradient products need: 1x128
+// along the columns (q, s: dX = D W) and along the rows (qt, st: dW = D^T X), as
+// fp8q_quant_act_dual makes them.  D itself is never written: 6 bytes read per element of
+// h and 4 written, against 6 + 4 + 4 + 4 for an elementwise pass followed by the quantizer.
+// Rows past M read as zeros, so qt and st cover M rounded up to 128 rows (zero codes,
+// which add nothing to dW).
+//
+// Grid: one block of 256 threads per 128 x 128 tile of h, columns fastest.  The three bf16
+// input tiles come by TMA (two boxes of 64 columns each); dg replaces g and du replaces u in
+// shared memory, and each is then quantized by the row and column passes of the quantizer.
+constexpr int kGatedBwdSmem = 3 * kDualTileBytes + 16 + 1024;
+constexpr unsigned int kSiteGatedBwd = 10;
+
+struct GatedBwdArgs {
+  uint8_t* q;           // [M, 2N]
+  float* s;             // [2N / 128][ld_s]
+  uint8_t* qt;          // [2N, ceil128(M)]
+  float* st;            // [ceil(M / 128)][ld_st]
+  int64_t ldq, ld_s, ldqt, ld_st, M, N;
+};
+
+// dg and du of one bf16 pair each, from words of dh, g and u.
+__device__ __forceinline__ void gated_grad_pair(uint32_t d, uint32_t& g, uint32_t& u) {
+  auto one = [](float dh, float gv, float uv, float& dg, float& du) {
+    const float sg = __fdividef(1.0f, 1.0f + __expf(-gv));
+    const float ds = dh * sg;
+    du = ds * gv;
+    dg = ds * uv * fmaf(gv, 1.0f - sg, 1.0f);
+  };
+  float2 dg, du;
+  one(bf16lo(d), bf16lo(g), bf16lo(u), dg.x, du.x);
+  one(bf16hi(d), bf16hi(g), bf16hi(u), dg.y, du.y);
+  __nv_bfloat162 a = __float22bfloat162_rn(dg), b = __float22bfloat162_rn(du);
+  g = *reinterpret_cast<uint32_t*>(&a);
+  u = *reinterpret_cast<uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool POW2>
+__global__ void __launch_bounds__(256, 2)
+    gated_backward_quant_kernel(const __grid_constant__ CUtensorMap tmDh, const __grid_constant__ CUtensorMap tmGu,
+                                const GatedBwdArgs p) {
+  extern __shared__ uint8_t gbwd_raw[];
+  const uint32_t tile = (smem_u32(gbwd_raw) + 1023u) & ~1023u;     // g, u, dh
+  const uint32_t bar = tile + 3 * kDualTileBytes;
+  const uint32_t nb = static_cast<uint32_t>(p.N / 128);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x % nb) * 128, m0 = static_cast<int64_t>(blockIdx.x / nb) * 128;
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, 3 * kDualTileBytes);
+    const int32_t y = static_cast<int32_t>(m0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t xg = static_cast<int32_t>(n0 + 64 * h), xu = static_cast<int32_t>(p.N + n0 + 64 * h);
+      const uint32_t at = tile + h * (kDualTileBytes / 2);
+      tma_load_2d(at, &tmGu, bar, xg, y);
+      tma_load_2d(at + kDualTileBytes, &tmGu, bar, xu, y);
+      tma_load_2d(at + 2 * kDualTileBytes, &tmDh, bar, xg, y);
+    }
+  }
+  // bounded (the loads end on their own); a timeout is recorded and the tile skipped
+  if (!__syncthreads_and(mbar_wait(bar, 0, kSiteGatedBwd, nullptr))) return;
+
+  // the elementwise part, in place (the tiles share one swizzle, so equal offsets are equal
+  // elements)
+#pragma unroll 2
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t at = tile + 16u * (threadIdx.x + 256 * j);
+    const uint4 d = ld_shared_v4(at + 2 * kDualTileBytes);
+    uint4 g = ld_shared_v4(at), u = ld_shared_v4(at + kDualTileBytes);
+    gated_grad_pair(d.x, g.x, u.x);
+    gated_grad_pair(d.y, g.y, u.y);
+    gated_grad_pair(d.z, g.z, u.z);
+    gated_grad_pair(d.w, g.w, u.w);
+    st_shared_v4(at, g);
+    st_shared_v4(at + kDualTileBytes, u);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l4 = lane & 3;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    const int64_t k0 = half * p.N + n0;
+    dual_rows_pass<POW2, true>(lane, warp, l4, tile + half * kDualTileBytes, m0, p.M, k0 / 128, k0, p.q, p.ldq, p.s, p.ld_s);
+    dual_columns_pass<POW2>(lane, warp, l4, tile + half * kDualTileBytes, m0, k0, p.qt, p.ldqt, p.st, p.ld_st);
+  }
+}
+
+}  // namespace fp8q

@@ -372,34 +372,14 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, u
                : "memory");
 }
 
-template <bool POW2>
-__global__ void __launch_bounds__(256, 6) quant_act_dual_kernel(const __grid_constant__ CUtensorMap tmx,
-                                                             uint8_t* __restrict__ q, int64_t ldq,
-                                                             float* __restrict__ s, int64_t lds,
-                                                             uint8_t* __restrict__ qt, int64_t ldqt,
-                                                             float* __restrict__ st, int64_t ldst,
-                                                             uint32_t G) {
-  extern __shared__ uint8_t dual_raw[];
-  const uint32_t tile = (smem_u32(dual_raw) + 1023u) & ~1023u;   // swizzle atoms need 1 KB
-  const uint32_t bar = tile + kDualTileBytes;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l4 = lane & 3;
-  const int64_t g = blockIdx.x % G, m0 = static_cast<int64_t>(blockIdx.x / G) * 128;
-  const int64_t k0 = g * 128;
-
-  if (threadIdx.x == 0) {
-    mbar_init(bar, 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    mbar_arrive_expect_tx(bar, kDualTileBytes);
-    tma_load_2d(tile, &tmx, bar, static_cast<int32_t>(k0), static_cast<int32_t>(m0));
-    tma_load_2d(tile + kDualTileBytes / 2, &tmx, bar, static_cast<int32_t>(k0 + 64), static_cast<int32_t>(m0));
-  }
-  // bounded (the loads end on their own); a timeout is recorded and the tile skipped
-  if (!__syncthreads_and(mbar_wait(bar, 0, kSiteDual, nullptr))) return;
-
+// The row pass over a 128x128 bf16 tile at shared address `tile` (rows m0.., columns k0..):
+// codes to q[m * ldq + k], scales to s[g * lds + m] (g = k0 / 128).  MASKED: rows from M on
+// are not written (the tile's row count is a multiple of 128 otherwise).  The thread's lane,
+// warp and l4 = lane % 4 are the caller's: computed again here they cost registers.
+template <bool POW2, bool MASKED>
+__device__ __forceinline__ void dual_rows_pass(int lane, int warp, int l4, uint32_t tile, int64_t m0, int64_t M, int64_t g, int64_t k0,
+                                               uint8_t* q, int64_t ldq,
+                                               float* s, int64_t lds) {
   // ---- rows: lane l4 of the team of row r holds chunks (l4 + 4 j + 4 (r & 1)) % 16
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -430,12 +410,19 @@ __global__ void __launch_bounds__(256, 6) quant_act_dual_kernel(const __grid_con
         uint2 o;
         o.x = __byte_perm(cvt_e4m3x2(p0.x, p0.y), cvt_e4m3x2(p1.x, p1.y), 0x5410);
         o.y = __byte_perm(cvt_e4m3x2(p2.x, p2.y), cvt_e4m3x2(p3.x, p3.y), 0x5410);
-        stg_u2(dst + 8 * cj[j], o);
+        if (!MASKED || m < M) stg_u2(dst + 8 * cj[j], o);
       }
     });
-    if (l4 == 0) s[g * lds + m] = sc;
+    if (l4 == 0 && (!MASKED || m < M)) s[g * lds + m] = sc;
   }
+}
 
+// The column pass over the same tile: codes to qt[k * ldqt + m], scales to
+// st[(m0 / 128) * ldst + k]; all 128 rows.
+template <bool POW2>
+__device__ __forceinline__ void dual_columns_pass(int lane, int warp, int l4, uint32_t tile, int64_t m0, int64_t k0,
+                                                  uint8_t* qt, int64_t ldqt,
+                                                  float* st, int64_t ldst) {
   // ---- columns 16 warp + 8 h + lane / 4 (h = 0, 1), all 128 rows
   const int quad = lane >> 2;                  // column inside the 8-column block
 #pragma unroll 1
@@ -481,6 +468,39 @@ __global__ void __launch_bounds__(256, 6) quant_act_dual_kernel(const __grid_con
                    __byte_perm(hi4[0], hi4[1], 0x7632), __byte_perm(hi4[2], hi4[3], 0x7632));
     if (l4 == 0) st[(m0 / 128) * ldst + col] = sc;
   }
+}
+
+template <bool POW2>
+__global__ void __launch_bounds__(256, 6) quant_act_dual_kernel(const __grid_constant__ CUtensorMap tmx,
+                                                             uint8_t* __restrict__ q, int64_t ldq,
+                                                             float* __restrict__ s, int64_t lds,
+                                                             uint8_t* __restrict__ qt, int64_t ldqt,
+                                                             float* __restrict__ st, int64_t ldst,
+                                                             uint32_t G) {
+  extern __shared__ uint8_t dual_raw[];
+  const uint32_t tile = (smem_u32(dual_raw) + 1023u) & ~1023u;   // swizzle atoms need 1 KB
+  const uint32_t bar = tile + kDualTileBytes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l4 = lane & 3;
+  const int64_t g = blockIdx.x % G, m0 = static_cast<int64_t>(blockIdx.x / G) * 128;
+  const int64_t k0 = g * 128;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, kDualTileBytes);
+    tma_load_2d(tile, &tmx, bar, static_cast<int32_t>(k0), static_cast<int32_t>(m0));
+    tma_load_2d(tile + kDualTileBytes / 2, &tmx, bar, static_cast<int32_t>(k0 + 64), static_cast<int32_t>(m0));
+  }
+  // bounded (the loads end on their own); a timeout is recorded and the tile skipped
+  if (!__syncthreads_and(mbar_wait(bar, 0, kSiteDual, nullptr))) return;
+
+  // every tile is whole here (M % 128 == 0)
+  dual_rows_pass<POW2, false>(lane, warp, l4, tile, m0, 0, g, k0, q, ldq, s, lds);
+  dual_columns_pass<POW2>(lane, warp, l4, tile, m0, k0, qt, ldqt, st, ldst);
 }
 
 // ---------------------------------------------------------------- transposed weight blocks

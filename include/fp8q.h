@@ -295,6 +295,87 @@ int fp8_gemm_nopromo(const uint8_t* A, const float* sA, const uint8_t* B, const 
                      int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                      void* stream);
 
+/*
+ * Per-row INT8 quantization of a bf16 matrix [M, K] (the operands of the INT8 products below:
+ * one scale per token for activations, one per output channel for weights).
+ *
+ * For every row m, with a = max_k |x[m, k]|:
+ *   a < 2^-100        s = 1 and q = 0 (a row of zeros, or of values that count as zero)
+ *   a Inf or NaN      s = NaN and q = 0, so that every product with the row is NaN
+ *   otherwise         s = RN_f32(a / 127), r = RN_f32(127 / a),
+ *                     q[m, k] = x[m, k] r rounded once to an integer, ties to even (|q| <= 127)
+ *   scales[m] = s
+ *
+ * x_bf16  device, bf16 [M, K], row stride ldx elements (K contiguous), any alignment
+ * q       device, int8 [M, K], row stride ldq bytes, any alignment
+ * scales  device, fp32 [M]
+ * Any K.  Rows that start on 16 bytes (codes: on 8) and K % 8 == 0 take the fastest path.
+ * Requires ldx >= K, ldq >= K, M <= 2^31 - 1.  Output is bit-exact with the definition.
+ */
+int fp8q_quant_int8_rowwise(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, int8_t* q,
+                            int64_t ldq, float* scales, void* stream);
+
+/*
+ * INT8 product scaled per token and per channel:
+ *   C[m, n] = RN_f32(RN_f32(RN_f32(acc) sA[m]) sB[n]),  acc = sum_k A[m, k] B[n, k]
+ * with acc exact (INT32), rounded once more for a bf16 C.
+ *
+ * A    device, int8 [M, K], row stride lda bytes      B    device, int8 [N, K], row stride ldb bytes
+ * sA   device, fp32 [M]                               sB   device, fp32 [N]
+ * C    device, bf16 or fp32 [M, N], row stride ldc elements
+ * Any M, N and K up to 131071 (K 128^2 <= 2^31 - 1; a longer K is FP8Q_ERR_SHAPE).  A and B
+ * start on 16 bytes and lda % 16 == ldb % 16 == 0 (columns K.. of the pitch are not read).
+ * C needs its elements' alignment only; rows that start on 16 bytes are stored fastest.
+ */
+int fp8q_gemm_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C,
+                   int out_dtype, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                   int64_t ldc, void* stream);
+
+/*
+ * Gated feed-forward projections in INT8: W holds 2N rows, the gate's N and then the up
+ * projection's N, sW their scales.  With C = the product above over all 2N rows,
+ *   H[m, n] = silu(g) u,  g = C[m, n], u = C[m, N + n],  silu(g) = g / (1 + exp(-g))
+ * in FP32, rounded once to bf16 (for g < -87.3 silu is returned as 0; it is above -1.2e-36).
+ * H device, bf16 [M, N], row stride ldh elements.  Everything else as fp8q_gemm_int8.
+ */
+int fp8q_gemm_int8_gated(const int8_t* A, const float* sA, const int8_t* W, const float* sW, void* H,
+                         int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw, int64_t ldh,
+                         void* stream);
+
+/*
+ * Gated feed-forward projections in block-scaled FP8 [K], [NC]: W [2N, K] holds the gate's N
+ * rows and then the up projection's N, quantized in 128x128 blocks.
+ *   g = A Wg^T, u = A Wu^T with the scaling and promotion of fp8_gemm_blockscaled (BLOCK mode),
+ *   H[m, n] = silu(g) u in FP32, rounded once to bf16 (silu as in fp8q_gemm_int8_gated).
+ * With GU, g and u rounded to bf16 are kept for the backward pass: GU[m, n] = g, GU[m, N + n] = u.
+ *
+ * A, sA   device, E4M3 [M, K] (row stride lda bytes), fp32 [K/128][ld_sa >= M]
+ * W, sW   device, E4M3 [2N, K] (row stride ldw bytes), fp32 [2N/128][K/128]
+ * H       device, bf16 [M, N], row stride ldh elements
+ * GU      device, bf16 [M, 2N], row stride ldgu elements, or NULL
+ * Shape and alignment rules of fp8_gemm_blockscaled (any M; N % 128 == K % 128 == 0).
+ */
+int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W,
+                               const float* sW, void* H, int64_t ldh, void* GU, int64_t ldgu,
+                               int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw,
+                               void* stream);
+
+/*
+ * Backward pass of the gated product, fused with the quantization of its result [Q], [P2].
+ * From dH [M, N] and GU [M, 2N] (g, then u), all bf16, with sg = 1 / (1 + exp(-g)):
+ *   dg = dH u sg (1 + g (1 - sg)),  du = dH g sg      in FP32, rounded to bf16,
+ * and of D = [dg | du] [M, 2N] (never written itself):
+ *   q, s     its 1x128 quantization (fp8q_quant_act_1x128): E4M3 [M, 2N], fp32 [2N/128][ld_s >= M]
+ *   qt, st   that of D^T with M rounded up to Mp = 128 ceil(M / 128), rows past M zero:
+ *            E4M3 [2N, Mp] (row stride ldqt bytes), fp32 [Mp/128][ld_st >= 2N]
+ * (q, s) is the left operand of dX = D W, (qt, st) that of dW = D^T X.
+ * Any M; N % 128 == 0; lddh, ldgu, ldq multiples of 8, ldqt of 16; dH, GU, qt 16-byte and q
+ * 8-byte aligned; ceil(M/128) * (N/128) <= 2^31 - 1.
+ */
+int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int64_t ldgu, int64_t M,
+                              int64_t N, uint8_t* q, int64_t ldq, float* s, int64_t ld_s, uint8_t* qt,
+                              int64_t ldqt, float* st, int64_t ld_st, int pow2_scale, void* stream);
+
 /* Reads and clears the device error word (synchronizes `stream`).  Returns 0 when no
  * device-side error was recorded, else (site << 8) | fp8q_status. */
 int fp8q_get_device_error(void* stream);
