@@ -3,12 +3,14 @@
 // library.cu's translation unit (after fp8q.cu, whose host helpers it uses).
 #include "gated.cuh"
 #include "int8.cuh"
+#include "skinny.cuh"
 
 namespace {
 
 using fp8q::GatedArgs;
 using fp8q::GatedBwdArgs;
 using fp8q::Int8Args;
+using fp8q::SkinnyArgs;
 
 // CTAs of `kern` that fit the current device at once; sets its shared memory limit on first
 // use.  0 on failure.
@@ -65,11 +67,97 @@ int int8_width(int64_t M, int64_t rows, bool gated, int units) {
   return best;
 }
 
+// Launch of the few-row kernel: `units` tiles of MP rows, K split over clusters of
+// `split` CTAs.
+template <int KIND, bool GATED, bool OUT_BF16, int MP>
+int launch_skinny(const CUtensorMap& tmA, const CUtensorMap& tmW, const SkinnyArgs& a, int64_t units,
+                  cudaStream_t stream) {
+  using Cfg = fp8q::SkinnyCfg<KIND, MP>;
+  static constexpr auto kern = fp8q::gemm_skinny_kernel<KIND, GATED, OUT_BF16, MP>;
+  if (resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes) <= 0) return FP8Q_ERR_CUDA;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(a.split);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * a.split));
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::smem_bytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmA, tmW, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+}
+
+// Rows of A per tile: the smallest that holds M, or the largest.
+int skinny_rows(int64_t M, int most) {
+  int mp = 16;
+  while (mp < M && mp < most) mp *= 2;
+  return mp;
+}
+
+// Clusters as wide as it takes to give every SM two CTAs, no wider than 8 CTAs (the portable
+// limit) or the K groups.
+int skinny_split(int64_t units, int64_t G, int sms) {
+  int64_t s = (2 * sms + units - 1) / units;
+  if (s > 8) s = 8;
+  if (s > G) s = G;
+  return static_cast<int>(s);
+}
+
+int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev].load(std::memory_order_acquire);
+  if (n) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  cached[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+// Rows up to which the few-row kernels run (see skinny.cuh).
+constexpr int64_t kSkinnyMaxRows = 128;
+
+// Fills in the tiling of the few-row kernel; returns its tile count, or 0 on failure.
+template <bool GATED>
+int64_t plan_skinny(SkinnyArgs* a, int mp, int sms) {
+  const int cols = GATED ? 64 : 128;
+  const int64_t nt = (a->N + cols - 1) / cols, units = nt * ((a->M + mp - 1) / mp);
+  if (units * 8 > 0x7FFFFFFF) return 0;
+  a->nt = static_cast<int>(nt);
+  a->split = skinny_split(units, a->G, sms);
+  return units;
+}
+
+template <bool GATED, bool OUT_BF16>
+int run_int8_skinny(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M, int64_t N,
+                    int64_t K, int64_t lda, int64_t ldb, int64_t ldc, cudaStream_t stream) {
+  constexpr int KIND = fp8q::kSkinnyInt8;
+  const int mp = skinny_rows(M, 128), sms = sm_count();
+  if (sms <= 0) return FP8Q_ERR_CUDA;
+  SkinnyArgs a{};
+  a.sA = sA; a.sB = sB; a.C = C; a.ldc = ldc; a.M = M; a.N = N; a.G = static_cast<int>((K + 127) / 128);
+  const int64_t units = plan_skinny<GATED>(&a, mp, sms);
+  if (units == 0) return FP8Q_ERR_SHAPE;
+  CUtensorMap tmA, tmW;
+  int st = encode_operand(&tmA, A, K, M, lda, mp);
+  if (st != FP8Q_OK || (st = encode_operand(&tmW, B, K, GATED ? 2 * N : N, ldb, GATED ? 64 : 128)) != FP8Q_OK) return st;
+  switch (mp) {
+    case 16: return launch_skinny<KIND, GATED, OUT_BF16, 16>(tmA, tmW, a, units, stream);
+    case 32: return launch_skinny<KIND, GATED, OUT_BF16, 32>(tmA, tmW, a, units, stream);
+    case 64: return launch_skinny<KIND, GATED, OUT_BF16, 64>(tmA, tmW, a, units, stream);
+    default: return launch_skinny<KIND, GATED, OUT_BF16, 128>(tmA, tmW, a, units, stream);
+  }
+}
+
 template <bool GATED, bool OUT_BF16>
 int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M, int64_t N,
              int64_t K, int64_t lda, int64_t ldb, int64_t ldc, void* stream) {
   using Cfg = fp8q::Int8Cfg;
   static constexpr auto kern = fp8q::gemm_int8_kernel<GATED, OUT_BF16>;
+  if (M <= kSkinnyMaxRows)
+    return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, static_cast<cudaStream_t>(stream));
   const int units = resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes);
   if (units <= 0) return FP8Q_ERR_CUDA;
   const int64_t rows = GATED ? 2 * N : N;
@@ -147,6 +235,26 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
   if (GU != nullptr) {
     if (ldgu < 2 * N) return FP8Q_ERR_SHAPE;
     if (ldgu % 8 != 0 || !aligned(GU, 16)) return FP8Q_ERR_ALIGN;
+  }
+  if (M <= kSkinnyMaxRows) {
+    constexpr int KIND = fp8q::kSkinnyFp8;
+    const int mp = skinny_rows(M, 64), sms = sm_count();
+    if (sms <= 0) return FP8Q_ERR_CUDA;
+    SkinnyArgs a{};
+    a.sA = sA; a.ld_sa = ld_sa; a.sB = sW; a.C = H; a.ldc = ldh;
+    a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+    const int64_t units = plan_skinny<true>(&a, mp, sms);
+    if (units == 0) return FP8Q_ERR_SHAPE;
+    CUtensorMap tmA, tmW;
+    if ((st = encode_operand(&tmA, A, K, M, lda, mp)) != FP8Q_OK ||
+        (st = encode_operand(&tmW, W, K, 2 * N, ldw, 64)) != FP8Q_OK)
+      return st;
+    const auto s = static_cast<cudaStream_t>(stream);
+    switch (mp) {
+      case 16: return launch_skinny<KIND, true, true, 16>(tmA, tmW, a, units, s);
+      case 32: return launch_skinny<KIND, true, true, 32>(tmA, tmW, a, units, s);
+      default: return launch_skinny<KIND, true, true, 64>(tmA, tmW, a, units, s);
+    }
   }
   GatedArgs a{};
   a.sA = sA; a.ld_sa = ld_sa; a.sW = sW;
