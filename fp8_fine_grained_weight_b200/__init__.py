@@ -507,24 +507,30 @@ def _ceil_to(n: int, multiple: int) -> int:
     return -(-n // multiple) * multiple
 
 
+def _new(rows: int, cols: int, dtype, device, pitch: Optional[int] = None) -> torch.Tensor:
+    """An uninitialized [rows, cols] tensor (empty_strided costs 0.8 us less than empty)."""
+    return torch.empty_strided((rows, cols), (cols if pitch is None else pitch, 1), dtype=dtype, device=device)
+
+
 def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """One scale per row: x bf16 [M, K] -> (q int8 [M, K], s fp32 [M]), x ~ q s.
 
     Per token for activations, per output channel for weights.  Any K; the codes' rows are
-    allocated 16 bytes apart or a multiple (q is a view of such a buffer when K % 16 != 0),
-    as the products need them.  A row that holds Inf or NaN gets the scale NaN.
+    allocated 16 bytes apart or a multiple (q is strided when K % 16 != 0), as the products
+    need them.  A row that holds Inf or NaN gets the scale NaN.
     """
     _need(x, torch.bfloat16, "x", 2)
     M, K = x.shape
     if K == 0:
         raise ValueError("x must have at least one column")
+    dev = x.device
     if out is None:
-        q = torch.empty((M, _ceil_to(K, 16)), dtype=torch.int8, device=x.device)[:, :K]
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+        q = _new(M, K, torch.int8, dev, _ceil_to(K, 16))
+        s = torch.empty_strided((M,), (1,), dtype=torch.float32, device=dev)
     else:
         q, s = out
-        _rows(q, torch.int8, "q", M, K, x.device)
-        _vector(s, "s", M, x.device)
+        _rows(q, torch.int8, "q", M, K, dev)
+        _vector(s, "s", M, dev)
     with _on(x):
         _call("fp8q_quant_int8_rowwise", x.data_ptr(), M, K, x.stride(0), q.data_ptr(), q.stride(0),
               s.data_ptr(), _stream(x))
@@ -541,6 +547,16 @@ def _vector(t: torch.Tensor, name: str, n: int, device: torch.device) -> None:
 
 def _int8_operands(qa, sa, qb, sb):
     """Checks of the INT8 products' operands; returns (M, rows of qb, K)."""
+    try:     # the checks below in one expression: a decode step's products are host-bound
+        dev = qa.get_device()
+        if (dev >= 0 and dev == qb.get_device() == sa.get_device() == sb.get_device()
+                and qa.dtype is qb.dtype is torch.int8 and sa.dtype is sb.dtype is torch.float32):
+            (M, K), (rows, Kb), (na,), (nb,) = qa.shape, qb.shape, sa.shape, sb.shape
+            if (K == Kb and na >= M and nb >= rows and qa.stride()[1] == qb.stride()[1] == 1
+                    and sa.stride()[0] == sb.stride()[0] == 1):
+                return M, rows, K
+    except (AttributeError, ValueError):
+        pass
     _need(qa, torch.int8, "qa", 2)
     _need(qb, torch.int8, "qb", 2)
     M, K = qa.shape
@@ -563,10 +579,11 @@ def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Te
     """
     M, N, K = _int8_operands(qa, sa, qb, sb)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+        code = _out_code(out_dtype)
+        out = _new(M, N, out_dtype, qa.device)
     else:
+        code = _out_code(out.dtype)
         _rows(out, out.dtype, "out", M, N, qa.device)
-    code = _out_code(out.dtype)
     with _on(qa):
         _call("fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
               out.data_ptr(), code, M, N, K, qa.stride(0), qb.stride(0), out.stride(0), _stream(qa))
@@ -585,7 +602,7 @@ def gemm_int8_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: to
         raise ValueError("qw must have an even number of rows: the gate's, then the up projection's")
     N = rows // 2
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
+        out = _new(M, N, torch.bfloat16, qa.device)
     else:
         _rows(out, torch.bfloat16, "out", M, N, qa.device)
     with _on(qa):
@@ -611,8 +628,8 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
         raise ValueError("qw must have 2N rows with N a multiple of 128")
     N = rows // 2
     if out is None:
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
-        gu = torch.empty((M, rows), dtype=torch.bfloat16, device=qa.device) if with_gu else None
+        h = _new(M, N, torch.bfloat16, qa.device)
+        gu = _new(M, rows, torch.bfloat16, qa.device) if with_gu else None
     else:
         _rows(h, torch.bfloat16, "h", M, N, qa.device)
         if with_gu:
@@ -642,10 +659,10 @@ def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False,
         raise ValueError("dh must have a multiple of 128 columns")
     Mp = _ceil_to(M, 128)
     if out is None:
-        q = torch.empty((M, 2 * N), dtype=torch.uint8, device=dev)
-        s = torch.empty((2 * N // 128, M), dtype=torch.float32, device=dev)
-        qt = torch.empty((2 * N, Mp), dtype=torch.uint8, device=dev)
-        st = torch.empty((Mp // 128, 2 * N), dtype=torch.float32, device=dev)
+        q = _new(M, 2 * N, torch.uint8, dev)
+        s = _new(2 * N // 128, M, torch.float32, dev)
+        qt = _new(2 * N, Mp, torch.uint8, dev)
+        st = _new(Mp // 128, 2 * N, torch.float32, dev)
     else:
         q, s, qt, st = out
         _rows(_u8(q), torch.uint8, "q", M, 2 * N, dev)

@@ -96,13 +96,13 @@ int skinny_rows(int64_t M, int most) {
   return mp;
 }
 
-// Clusters as wide as it takes to give every SM two CTAs, no wider than 8 CTAs (the portable
-// limit) or the K groups.
+// CTAs per cluster: as many as still fit two to an SM, at most four.  (16 x 7168 x 7168 INT8,
+// 56 tiles: 22.0 / 15.2 / 14.9 / 14.1 us for 1 to 4; 16.3, 18.0 and 17.6 us for 5, 6 and 8:
+// wider clusters leave SMs of a GPC without work.)
 int skinny_split(int64_t units, int64_t G, int sms) {
-  int64_t s = (2 * sms + units - 1) / units;
-  if (s > 8) s = 8;
-  if (s > G) s = G;
-  return static_cast<int>(s);
+  int s = fp8q::kMaxSplit;
+  while (s > 1 && (units * s > 2 * sms || s > G)) s /= 2;
+  return s;
 }
 
 int sm_count() {
@@ -116,8 +116,15 @@ int sm_count() {
   return n;
 }
 
-// Rows up to which the few-row kernels run (see skinny.cuh).
-constexpr int64_t kSkinnyMaxRows = 128;
+// Whether the few-row kernel takes the product: always up to its largest tile of rows, and beyond
+// that, up to 512 rows, while the wide kernel's 128 x 256 tiles would leave most SMs idle.
+// (us, few-row / wide.  INT8 N 7168 K 7168: 128 rows 17.5 / 23.0, 256 22.5 / 24.5, 512 34.5 /
+// 27.6.  INT8 gated N 2048 K 7168: 256 rows 16.5 / 22.2, 512 20.5 / 23.7, 1000 32.8 / 28.7.
+// FP8 gated N 2048 K 7168: 64 rows 12.3 / 34, 256 22.3 / 34.0, 512 37.2 / 34.0.)
+bool few_rows(int64_t M, int64_t rows, int sms, bool fp8) {
+  if (M <= (fp8 ? 64 : 128)) return true;
+  return M <= 512 && (M + 127) / 128 * ((rows + 255) / 256) * (fp8 ? 3 : 2) <= sms;
+}
 
 // Fills in the tiling of the few-row kernel; returns its tile count, or 0 on failure.
 template <bool GATED>
@@ -132,14 +139,15 @@ int64_t plan_skinny(SkinnyArgs* a, int mp, int sms) {
 
 template <bool GATED, bool OUT_BF16>
 int run_int8_skinny(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M, int64_t N,
-                    int64_t K, int64_t lda, int64_t ldb, int64_t ldc, cudaStream_t stream) {
+                    int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int sms, cudaStream_t stream) {
   constexpr int KIND = fp8q::kSkinnyInt8;
-  const int mp = skinny_rows(M, 128), sms = sm_count();
-  if (sms <= 0) return FP8Q_ERR_CUDA;
+  const int mp = skinny_rows(M, 128);
   SkinnyArgs a{};
   a.sA = sA; a.sB = sB; a.C = C; a.ldc = ldc; a.M = M; a.N = N; a.G = static_cast<int>((K + 127) / 128);
   const int64_t units = plan_skinny<GATED>(&a, mp, sms);
   if (units == 0) return FP8Q_ERR_SHAPE;
+  constexpr int kVecBytes = OUT_BF16 ? 8 : 16;
+  a.vec = (ldc * (OUT_BF16 ? 2 : 4)) % kVecBytes == 0 && aligned(C, kVecBytes);
   CUtensorMap tmA, tmW;
   int st = encode_operand(&tmA, A, K, M, lda, mp);
   if (st != FP8Q_OK || (st = encode_operand(&tmW, B, K, GATED ? 2 * N : N, ldb, GATED ? 64 : 128)) != FP8Q_OK) return st;
@@ -156,8 +164,11 @@ int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
              int64_t K, int64_t lda, int64_t ldb, int64_t ldc, void* stream) {
   using Cfg = fp8q::Int8Cfg;
   static constexpr auto kern = fp8q::gemm_int8_kernel<GATED, OUT_BF16>;
-  if (M <= kSkinnyMaxRows)
-    return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, static_cast<cudaStream_t>(stream));
+  const int sms = sm_count();
+  if (sms <= 0) return FP8Q_ERR_CUDA;
+  if (few_rows(M, GATED ? 2 * N : N, sms, false))
+    return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, sms,
+                                            static_cast<cudaStream_t>(stream));
   const int units = resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes);
   if (units <= 0) return FP8Q_ERR_CUDA;
   const int64_t rows = GATED ? 2 * N : N;
@@ -236,13 +247,15 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
     if (ldgu < 2 * N) return FP8Q_ERR_SHAPE;
     if (ldgu % 8 != 0 || !aligned(GU, 16)) return FP8Q_ERR_ALIGN;
   }
-  if (M <= kSkinnyMaxRows) {
+  const int sms = sm_count();
+  if (sms <= 0) return FP8Q_ERR_CUDA;
+  if (few_rows(M, 2 * N, sms, true)) {
     constexpr int KIND = fp8q::kSkinnyFp8;
-    const int mp = skinny_rows(M, 64), sms = sm_count();
-    if (sms <= 0) return FP8Q_ERR_CUDA;
+    const int mp = skinny_rows(M, 64);
     SkinnyArgs a{};
     a.sA = sA; a.ld_sa = ld_sa; a.sB = sW; a.C = H; a.ldc = ldh;
     a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+    a.vec = 1;
     const int64_t units = plan_skinny<true>(&a, mp, sms);
     if (units == 0) return FP8Q_ERR_SHAPE;
     CUtensorMap tmA, tmW;

@@ -42,8 +42,11 @@ struct SkinnyArgs {
   int64_t ld_gu, M, N;
   int G;                // groups of 128 K-elements
   int nt;               // weight tiles
-  int split;            // CTAs per cluster
+  int split;            // CTAs per cluster, at most kMaxSplit
+  int vec;              // C takes four elements at a time
 };
+
+constexpr int kMaxSplit = 4;
 
 template <int KIND, int MP>
 struct SkinnyCfg {
@@ -69,10 +72,16 @@ struct SkinnyCfg {
   static_assert(KIND == kSkinnyInt8 || MP <= 64, "FP8 keeps MP running sums in registers");
 };
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint2 bf16x4(const float (&v)[4]) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
 // TMEM columns of this warp's lanes into registers, by the count.
@@ -282,44 +291,71 @@ __global__ void __launch_bounds__(256, 2)
   cluster_sync();
 
   // ------------------------------------------------------------------ sum and finish
+  // Four consecutive columns of a row per thread and step, so that few steps wait for the
+  // other CTAs' shared memory.
   const int rows = static_cast<int>(p.M - row0 < MP ? p.M - row0 : MP);
   const uint32_t part_u32 = sbase + Cfg::part;
-  auto total = [&](int m, int r) {                         // over the cluster, in CTA order
-    uint32_t v[8];
+  auto total = [&](int m, int r, float (&t)[4]) {          // over the cluster, in CTA order
+    uint4 v[kMaxSplit];
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
-      v[s] = s < p.split ? ld_cluster_u32(map_shared_rank(part_u32 + 4u * (128 * m + r), s)) : 0u;
-    if constexpr (FP8) {
-      float t = __uint_as_float(v[0]);
+    for (int s = 0; s < kMaxSplit; ++s)
+      v[s] = s < p.split ? ld_cluster_v4(map_shared_rank(part_u32 + 4u * (128 * m + r), s)) : make_uint4(0, 0, 0, 0);
+    uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-      for (int s = 1; s < 8; ++s) t += __uint_as_float(v[s]);
-      return t;
-    } else {
-      uint32_t t = v[0];
+    for (int s = 1; s < kMaxSplit; ++s) {
+      const uint32_t a[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
 #pragma unroll
-      for (int s = 1; s < 8; ++s) t += v[s];
-      return __int2float_rn(static_cast<int>(t));
+      for (int j = 0; j < 4; ++j)
+        w[j] = FP8 ? __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(a[j])) : w[j] + a[j];
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = FP8 ? __uint_as_float(w[j]) : __int2float_rn(static_cast<int>(w[j]));
   };
-  for (int e = rank * Cfg::kThreads + threadIdx.x; e < rows * kCols; e += p.split * Cfg::kThreads) {
-    const int m = e / kCols, c = e % kCols;
+  for (int e = rank * Cfg::kThreads + threadIdx.x; e < rows * (kCols / 4); e += p.split * Cfg::kThreads) {
+    const int m = e / (kCols / 4), c = 4 * (e % (kCols / 4));
     const int64_t n = col0 + c, row = row0 + m;
-    if (n >= p.N) continue;
-    float v = total(m, c);
-    if constexpr (!FP8) v = (v * __ldg(p.sA + row)) * __ldg(p.sB + n);
+    const int left = static_cast<int>(p.N - n < 4 ? p.N - n : 4);
+    if (left <= 0) continue;
+    float v[4], u[4];
+    total(m, c, v);
+    if constexpr (GATED) total(m, 64 + c, u);
+    if constexpr (!FP8) {
+      const float sa = __ldg(p.sA + row);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < left) v[j] = (v[j] * sa) * __ldg(p.sB + n + j);
+        if (GATED && j < left) u[j] = (u[j] * sa) * __ldg(p.sB + p.N + n + j);
+      }
+    }
     if constexpr (GATED) {
-      float u = total(m, 64 + c);
-      if constexpr (!FP8) u = (u * __ldg(p.sA + row)) * __ldg(p.sB + p.N + n);
       if constexpr (FP8) {
-        if (p.gu != nullptr) {
-          p.gu[row * p.ld_gu + n] = __float2bfloat16_rn(v);
-          p.gu[row * p.ld_gu + p.N + n] = __float2bfloat16_rn(u);
+        if (p.gu != nullptr) {                             // N % 128 == 0, rows on 16 bytes
+          *reinterpret_cast<uint2*>(p.gu + row * p.ld_gu + n) = bf16x4(v);
+          *reinterpret_cast<uint2*>(p.gu + row * p.ld_gu + p.N + n) = bf16x4(u);
         }
       }
-      v = silu_mul(v, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = silu_mul(v[j], u[j]);
     }
-    if (OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[row * p.ldc + n] = __float2bfloat16_rn(v);
-    else reinterpret_cast<float*>(p.C)[row * p.ldc + n] = v;
+    if (OUT_BF16) {
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.C) + row * p.ldc + n;
+      if (p.vec && left == 4) {
+        *reinterpret_cast<uint2*>(out) = bf16x4(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < left) out[j] = __float2bfloat16_rn(v[j]);
+      }
+    } else {
+      float* out = reinterpret_cast<float*>(p.C) + row * p.ldc + n;
+      if (p.vec && left == 4) {
+        *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < left) out[j] = v[j];
+      }
+    }
   }
 
   // ---------------------------------------------------------------- teardown
