@@ -1,6 +1,8 @@
 // Entry points of the 8-bit feed-forward operators declared in include/fp8q.h: per-row INT8
 // quantization, INT8 products, and the gated projections with their backward pass.  Part of
 // library.cu's translation unit (after fp8q.cu, whose host helpers it uses).
+#include <algorithm>
+
 #include "gated.cuh"
 #include "int8.cuh"
 #include "skinny.cuh"
@@ -51,18 +53,28 @@ int check_int8(const int8_t* A, const float* sA, const int8_t* B, const float* s
   return FP8Q_OK;
 }
 
-// Columns of B per tile: the width with the least time over all waves.  A tile's time per
-// K step is the larger of its products (width / 2 cycles at 8192 products a cycle) and its
-// operands' way out of shared memory ((128 + width) / 4 cycles at 128 bytes a cycle).
-int int8_width(int64_t M, int64_t rows, bool gated, int units) {
+// Tiling of the wide INT8 kernel: CTA pairs or single CTAs, and columns of B per tile, by the
+// least time over all waves.  A tile's time per 128 K-elements, in ns, fitted to measurements
+// with K = 7168: single CTAs 296 / 293 / 313 / 305 / 350 / 374 / 384 for widths 64, 96, 128, 160,
+// 192, 224 and 256 (up to 64 bytes a cycle from L2), pairs 305 / 304 / 304 / 309 / 320 / 350 /
+// 355.  Below a width of 160 the four dependent products of a stage, 70 ns each, set the time.
+struct Int8Tiling {
+  bool pair;
+  int width;
+};
+
+Int8Tiling int8_tiling(int64_t M, int64_t rows, bool gated, int sms) {
   const int step = gated ? 64 : 32;
-  const int64_t mt = (M + 127) / 128;
-  int best = 256;
+  Int8Tiling best{false, 256};
   int64_t best_cost = INT64_MAX;
-  for (int w = 256; w >= step; w -= step) {
-    const int64_t waves = (mt * ((rows + w - 1) / w) + units - 1) / units;
-    const int64_t cost = waves * (2 * w > 128 + w ? 2 * w : 128 + w);
-    if (cost < best_cost) best = w, best_cost = cost;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int64_t mt = pair ? (M + 255) / 256 : (M + 127) / 128;
+    const int units = pair ? sms / 2 : sms;
+    for (int w = 256; w >= step; w -= step) {
+      const int64_t waves = (mt * ((rows + w - 1) / w) + units - 1) / units;
+      const int64_t cost = waves * (pair ? std::max(30500, 21500 + 54 * w) : std::max(29600, 21000 + 68 * w));
+      if (cost < best_cost) best = {pair != 0, w}, best_cost = cost;
+    }
   }
   return best;
 }
@@ -159,36 +171,56 @@ int run_int8_skinny(const int8_t* A, const float* sA, const int8_t* B, const flo
   }
 }
 
+template <bool GATED, bool OUT_BF16, bool PAIR>
+int launch_int8(const CUtensorMap& tmA, const CUtensorMap& tmB, Int8Args a, int sms, cudaStream_t stream) {
+  using Cfg = fp8q::Int8Cfg<PAIR>;
+  static constexpr auto kern = fp8q::gemm_int8_kernel<GATED, OUT_BF16, PAIR>;
+  if (resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes) <= 0) return FP8Q_ERR_CUDA;
+  a.stages = Cfg::stages(a.width);
+  const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt;
+  constexpr int cg = PAIR ? 2 : 1;
+  const int64_t units = tiles < sms / cg ? tiles : sms / cg;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cg;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * cg));
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::smem_bytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+}
+
 template <bool GATED, bool OUT_BF16>
 int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M, int64_t N,
-             int64_t K, int64_t lda, int64_t ldb, int64_t ldc, void* stream) {
-  using Cfg = fp8q::Int8Cfg;
-  static constexpr auto kern = fp8q::gemm_int8_kernel<GATED, OUT_BF16>;
+             int64_t K, int64_t lda, int64_t ldb, int64_t ldc, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return FP8Q_ERR_CUDA;
-  if (few_rows(M, GATED ? 2 * N : N, sms, false))
-    return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, sms,
-                                            static_cast<cudaStream_t>(stream));
-  const int units = resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes);
-  if (units <= 0) return FP8Q_ERR_CUDA;
   const int64_t rows = GATED ? 2 * N : N;
+  if (few_rows(M, rows, sms, false))
+    return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, sms, stream);
+  const Int8Tiling t = int8_tiling(M, rows, GATED, sms);
   Int8Args a{};
   a.sA = sA; a.sB = sB; a.C = C; a.ldc = ldc; a.M = M; a.N = N;
   a.k_groups = static_cast<int>((K + 127) / 128);
-  a.width = int8_width(M, rows, GATED, units);
-  const int cols = GATED ? a.width / 2 : a.width;
-  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + cols - 1) / cols;
+  a.width = t.width;
+  const int cols = GATED ? a.width / 2 : a.width, tile_m = t.pair ? 256 : 128;
+  const int64_t mt = (M + tile_m - 1) / tile_m, nt = (N + cols - 1) / cols;
   if (mt * nt > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
   a.mt = static_cast<int>(mt);
   a.nt = static_cast<int>(nt);
   a.n_fastest = M > rows;
   a.vec = (ldc * (OUT_BF16 ? 2 : 4)) % 16 == 0 && aligned(C, 16);
   CUtensorMap tmA, tmB;
-  int st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM);
-  if (st != FP8Q_OK || (st = encode_operand(&tmB, B, K, rows, ldb, cols)) != FP8Q_OK) return st;
-  const int64_t grid = mt * nt < units ? mt * nt : units;
-  kern<<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::smem_bytes, static_cast<cudaStream_t>(stream)>>>(tmA, tmB, a);
-  return launched();
+  int st = encode_operand(&tmA, A, K, M, lda, 128);
+  // a box of B: the tile's rows of one CTA (gated: of one projection)
+  if (st != FP8Q_OK || (st = encode_operand(&tmB, B, K, rows, ldb, GATED || t.pair ? a.width / 2 : a.width)) != FP8Q_OK)
+    return st;
+  return t.pair ? launch_int8<GATED, OUT_BF16, true>(tmA, tmB, a, sms, stream)
+                : launch_int8<GATED, OUT_BF16, false>(tmA, tmB, a, sms, stream);
 }
 
 }  // namespace
@@ -222,8 +254,9 @@ int fp8q_gemm_int8(const int8_t* A, const float* sA, const int8_t* B, const floa
   if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
   const int st = check_int8(A, sA, B, sB, C, out_dtype, M, N, K, lda, ldb, ldc);
   if (st != FP8Q_OK) return st;
-  return out_dtype == FP8Q_OUT_BF16 ? run_int8<false, true>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, stream)
-                                    : run_int8<false, false>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, stream);
+  const auto s = static_cast<cudaStream_t>(stream);
+  return out_dtype == FP8Q_OUT_BF16 ? run_int8<false, true>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, s)
+                                    : run_int8<false, false>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, s);
 }
 
 int fp8q_gemm_int8_gated(const int8_t* A, const float* sA, const int8_t* W, const float* sW, void* H, int64_t M,
@@ -231,7 +264,7 @@ int fp8q_gemm_int8_gated(const int8_t* A, const float* sA, const int8_t* W, cons
   if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
   const int st = check_int8(A, sA, W, sW, H, FP8Q_OUT_BF16, M, N, K, lda, ldw, ldh);
   if (st != FP8Q_OK) return st;
-  return run_int8<true, true>(A, sA, W, sW, H, M, N, K, lda, ldw, ldh, stream);
+  return run_int8<true, true>(A, sA, W, sW, H, M, N, K, lda, ldw, ldh, static_cast<cudaStream_t>(stream));
 }
 
 int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W, const float* sW,
@@ -326,12 +359,13 @@ int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int6
   const auto grid = static_cast<unsigned>(mt * (N / 128));
   const auto stm = static_cast<cudaStream_t>(stream);
   static constexpr auto k1 = fp8q::gated_backward_quant_kernel<true>, k0 = fp8q::gated_backward_quant_kernel<false>;
-  if ((pow2_scale ? resident_ctas<k1>(256, fp8q::kGatedBwdSmem) : resident_ctas<k0>(256, fp8q::kGatedBwdSmem)) <= 0)
+  constexpr int T = fp8q::kGatedBwdThreads;
+  if ((pow2_scale ? resident_ctas<k1>(T, fp8q::kGatedBwdSmem) : resident_ctas<k0>(T, fp8q::kGatedBwdSmem)) <= 0)
     return FP8Q_ERR_CUDA;
   if (pow2_scale)
-    k1<<<grid, 256, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
+    k1<<<grid, T, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
   else
-    k0<<<grid, 256, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
+    k0<<<grid, T, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
   return launched();
 }
 

@@ -325,9 +325,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // Rows past M read as zeros, so qt and st cover M rounded up to 128 rows (zero codes,
 // which add nothing to dW).
 //
-// Grid: one block of 256 threads per 128 x 128 tile of h, columns fastest.  The three bf16
-// input tiles come by TMA (two boxes of 64 columns each); dg replaces g and du replaces u in
-// shared memory, and each is then quantized by the row and column passes of the quantizer.
+// Grid: one block of 512 threads per 128 x 128 tile of h, columns fastest, two to an SM.  The
+// three bf16 input tiles come by TMA (two boxes of 64 columns each); dg replaces g and du
+// replaces u in shared memory, and each is then quantized by the row and column passes of the
+// quantizer, dg by the first eight warps and du by the others.
+constexpr int kGatedBwdThreads = 512;
 constexpr int kGatedBwdSmem = 3 * kDualTileBytes + 16 + 1024;
 constexpr unsigned int kSiteGatedBwd = 10;
 
@@ -363,7 +365,7 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 
 template <bool POW2>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kGatedBwdThreads, 2)
     gated_backward_quant_kernel(const __grid_constant__ CUtensorMap tmDh, const __grid_constant__ CUtensorMap tmGu,
                                 const GatedBwdArgs p) {
   extern __shared__ uint8_t gbwd_raw[];
@@ -394,8 +396,8 @@ __global__ void __launch_bounds__(256, 2)
   // the elementwise part, in place (the tiles share one swizzle, so equal offsets are equal
   // elements)
 #pragma unroll 2
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t at = tile + 16u * (threadIdx.x + 256 * j);
+  for (int j = 0; j < 2048 / kGatedBwdThreads; ++j) {
+    const uint32_t at = tile + 16u * (threadIdx.x + kGatedBwdThreads * j);
     const uint4 d = ld_shared_v4(at + 2 * kDualTileBytes);
     uint4 g = ld_shared_v4(at), u = ld_shared_v4(at + kDualTileBytes);
     gated_grad_pair(d.x, g.x, u.x);
@@ -406,13 +408,12 @@ __global__ void __launch_bounds__(256, 2)
     st_shared_v4(at + kDualTileBytes, u);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l4 = lane & 3;
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    const int64_t k0 = half * p.N + n0;
-    dual_rows_pass<POW2, true>(lane, warp, l4, tile + half * kDualTileBytes, m0, p.M, k0 / 128, k0, p.q, p.ldq, p.s, p.ld_s);
-    dual_columns_pass<POW2>(lane, warp, l4, tile + half * kDualTileBytes, m0, k0, p.qt, p.ldqt, p.st, p.ld_st);
-  }
+  const int lane = threadIdx.x & 31, l4 = lane & 3;
+  const int half = threadIdx.x >> 8, warp = (threadIdx.x >> 5) & 7;
+  const uint32_t mine = tile + half * kDualTileBytes;
+  const int64_t k0 = half * p.N + n0;
+  dual_rows_pass<POW2, true>(lane, warp, l4, mine, m0, p.M, k0 / 128, k0, p.q, p.ldq, p.s, p.ld_s);
+  dual_columns_pass<POW2>(lane, warp, l4, mine, m0, k0, p.qt, p.ldqt, p.st, p.ld_st);
 }
 
 }  // namespace fp8q

@@ -184,12 +184,20 @@ __global__ void __launch_bounds__(kInt8Threads)
 // Tiles of 128 rows by `width` columns (a launch parameter, at most 256, chosen by the host
 // so that the last wave is as full as it can be), persistent CTAs of 12 warps:
 //   warp 0      TMA producer: A [128 x 128 B] and B [width x 128 B] per 128 K-elements into
-//               a 4-stage ring (128-byte swizzle).  K past the operand's end is filled with
-//               zeros.  GATED: width / 2 gate rows, then width / 2 up rows.
+//               a ring of as many stages as fit (4 at width 256, up to 8; 128-byte swizzle):
+//               a narrow tile's products are over sooner, and its operands must be further
+//               ahead.  K past the operand's end is filled with zeros.  GATED: width / 2 gate
+//               rows, then width / 2 up rows.
 //   warp 1      TMEM owner and MMA issuer: 4 x tcgen05.mma kind::i8 (M128, K32) per stage.
 //   warps 2, 3  idle.
 //   warps 4-11  epilogue: warp w reads TMEM lanes 32 (w % 4).. in chunks of 32 columns, the
 //               chunks alternating between the two warpgroups.
+//
+// PAIR: two CTAs share a tile of 256 rows (cta_group::2).  Each loads and holds its 128 rows of
+// A and half the tile's rows of B (GATED: one the gate's, the other the up projection's), and
+// the first issues MMAs of M = 256 that leave each CTA its own rows' sums.  An SM takes in at
+// most 64 bytes a cycle from L2; a 128 x 256 tile alone needs 48 KB per 512-cycle stage, half
+// as much again, a paired one 32 KB.
 struct Int8Args {
   const float* sA;      // [M]
   const float* sB;      // [N], gated [2N]
@@ -197,6 +205,7 @@ struct Int8Args {
   int64_t ldc, M, N;
   int k_groups;         // ceil(K / 128)
   int width;            // B rows per tile: a multiple of 32 (gated: of 64), at most 256
+  int stages;           // Int8Cfg::stages(width)
   int mt, nt;           // tiles along M and N
   int n_fastest;
   int vec;              // C's rows start on 16 bytes
@@ -208,15 +217,24 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, S8 x S8 -> S32, one CTA.
+// D[tmem] (+)= A[smem] * B[smem]^T, S8 x S8 -> S32.  CG = 2: a CTA pair, as in mma_f8.
+template <int CG>
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // silu(g) u.  For g < -87.3 the divisor passes 2^126 and the quotient is returned as 0;
@@ -286,28 +304,39 @@ __device__ __forceinline__ void store_chunk32(uint32_t (&v)[32], void* C, int64_
   }
 }
 
+template <bool PAIR>
 struct Int8Cfg {
-  static constexpr int kTileM = 128, kMaxWidth = 256, kStages = 4;
+  static constexpr int kTileM = PAIR ? 256 : 128, kMaxWidth = 256, kMaxStages = 8;
   static constexpr int kThreads = 32 * (4 + 8);
-  static constexpr uint32_t kABytes = 128 * kBK, kBBytes = kMaxWidth * kBK;
-  static constexpr uint32_t a = 0;
-  static constexpr uint32_t b = a + kStages * kABytes;
-  static constexpr uint32_t scales = b + kStages * kBBytes;           // float[2][kMaxWidth]
+  static constexpr uint32_t kABytes = 128 * kBK;
+  static constexpr uint32_t kRingBytes = 4 * (kABytes + kMaxWidth * kBK);
+  static constexpr uint32_t ring = 0;                                  // a stage: A, then B
+  static constexpr uint32_t scales = ring + kRingBytes;                // float[2][kMaxWidth]
   static constexpr uint32_t bars = scales + 2 * kMaxWidth * 4;
-  // full[S], empty[S], tfull[2], tempty[2], drain
-  static constexpr uint32_t misc = align_up(bars + 8 * (2 * kStages + 5), 16);
+  // full[8], empty[8], tfull[2], tempty[2], drain
+  static constexpr uint32_t misc = align_up(bars + 8 * (2 * kMaxStages + 5), 16);
   static constexpr uint32_t smem_bytes = misc + 16 + 1024;
   static_assert(smem_bytes <= 232448, "fits the 227 KB opt-in shared memory");
+  // of one CTA: its 128 rows of A and its share of B
+  static constexpr __host__ __device__ uint32_t stage_bytes(int width) {
+    return kABytes + (PAIR ? width / 2 : width) * kBK;
+  }
+  static constexpr int stages(int width) {
+    const int n = kRingBytes / stage_bytes(width);
+    return n < kMaxStages ? n : kMaxStages;
+  }
 };
 
-template <bool GATED, bool OUT_BF16>
-__global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
+template <bool GATED, bool OUT_BF16, bool PAIR>
+__global__ void __launch_bounds__(Int8Cfg<PAIR>::kThreads, 1)
     gemm_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const Int8Args p) {
   static_assert(OUT_BF16 || !GATED, "the gated product is bf16");
-  using Cfg = Int8Cfg;
-  constexpr int S = Cfg::kStages;
+  using Cfg = Int8Cfg<PAIR>;
+  constexpr int CG = PAIR ? 2 : 1;
+  constexpr int S = Cfg::kMaxStages;                       // barriers; the ring has p.stages
   extern __shared__ uint8_t smem_raw[];
+  // (the pair's CTAs have the same layout: shared memory starts at the same offset in both)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -322,8 +351,10 @@ __global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::misc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;      // 0: the CTA that issues the MMAs
+  const int unit0 = blockIdx.x / CG, units = gridDim.x / CG;
   const int G = p.k_groups;
-  const int cols = GATED ? p.width / 2 : p.width;        // output columns per tile
+  const int cols = GATED ? p.width / 2 : p.width;          // output columns per tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -332,7 +363,7 @@ __global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 32 * kEpiWarps);
+      mbar_init(tempty_bar(b), CG * 32 * kEpiWarps);       // the pair's epilogues free rank 0's
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -343,79 +374,98 @@ __global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish<1>();
+    tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish<CG>();
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                                // both CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   const int tiles = p.mt * p.nt;
-  const int n_tiles = (tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int n_tiles = unit0 < tiles ? (tiles - unit0 + units - 1) / units : 0;
   auto tile_at = [&](int i, int64_t& row0, int64_t& col0) {
-    const int t = blockIdx.x + i * gridDim.x;
+    const int t = unit0 + i * units;
     const int fast = p.n_fastest ? p.nt : p.mt;
     const int q = t / fast, r = t - q * fast;
-    row0 = static_cast<int64_t>(p.n_fastest ? q : r) * Cfg::kTileM;
+    row0 = static_cast<int64_t>(p.n_fastest ? q : r) * Cfg::kTileM + 128 * rank;
     col0 = static_cast<int64_t>(p.n_fastest ? r : q) * cols;
   };
 
   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      const uint32_t tx = Cfg::kABytes + static_cast<uint32_t>(p.width) * kBK;
-      uint32_t it = 0;
+      const uint32_t stage = Cfg::stage_bytes(p.width);
+      uint32_t it = 0, phase = 1;                          // of the empty barriers
+      int s = 0;
       bool ok = true;
       for (int i = 0; ok && i < n_tiles; ++i) {
         int64_t row0, col0;
         tile_at(i, row0, col0);
         for (int g = 0; g < G; ++g, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(empty_bar(s), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) {
+          if (!mbar_wait(empty_bar(s), phase, kSiteProducer, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(full_bar(s), tx);
-          const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
-          tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), g * kBK, static_cast<int32_t>(row0));
-          tma_load_2d(b_addr, &tmB, full_bar(s), g * kBK, static_cast<int32_t>(col0));
-          if (GATED)
-            tma_load_2d(b_addr + cols * kBK, &tmB, full_bar(s), g * kBK, static_cast<int32_t>(p.N + col0));
+          const uint32_t a_addr = sbase + Cfg::ring + s * stage, b_addr = a_addr + Cfg::kABytes;
+          const int32_t x = g * kBK, ya = static_cast<int32_t>(row0), yb = static_cast<int32_t>(col0);
+          if constexpr (PAIR) {
+            // both CTAs' bytes count on rank 0's barrier, whose phase its own arrival opens
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * stage);
+            const uint32_t bar = map_shared_rank(full_bar(s), 0);
+            tma_load_2d_pair(a_addr, &tmA, bar, x, ya);
+            tma_load_2d_pair(b_addr, &tmB, bar, x,
+                             rank == 0 ? yb : static_cast<int32_t>(GATED ? p.N + col0 : col0 + p.width / 2));
+          } else {
+            mbar_arrive_expect_tx(full_bar(s), stage);
+            tma_load_2d(a_addr, &tmA, full_bar(s), x, ya);
+            tma_load_2d(b_addr, &tmB, full_bar(s), x, yb);
+            if (GATED) tma_load_2d(b_addr + cols * kBK, &tmB, full_bar(s), x, static_cast<int32_t>(p.N + col0));
+          }
+          if (++s == p.stages) s = 0, phase ^= 1;
         }
       }
-      // every issued load lands before the CTA can exit (bounded; loads end on their own)
-      const uint32_t first = it > static_cast<uint32_t>(S) ? it - S : 0;
-      for (uint32_t j = first; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
+      // Every issued load lands before the CTA can exit: rank 0 sees its stages' bytes arrive, rank
+      // 1 sees their products, which waited for them, complete (bounded; loads end on their
+      // own).
+      const uint32_t n = p.stages;
+      for (uint32_t j = it > n ? it - n : 0; j < it; ++j)
+        mbar_wait(rank == 0 ? full_bar(j % n) : empty_bar(j % n), (j / n) & 1u, kSiteDrain, nullptr);
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_s8_s32(Cfg::kTileM, p.width);
-      uint32_t it = 0;
+      const uint32_t stage = Cfg::stage_bytes(p.width);
+      auto commit = [&](uint32_t bar) {
+        if constexpr (PAIR) mma_commit_pair(bar, 3);
+        else mma_commit<1>(bar);
+      };
+      uint32_t phase = 0;                                  // of the full barriers
+      int s = 0;
       bool ok = true;
       for (int i = 0; ok && i < n_tiles; ++i) {
         const uint32_t buf = i & 1;
         if (!mbar_wait(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
         const uint32_t d = tmem_base + buf * Cfg::kMaxWidth;
-        for (int g = 0; g < G; ++g, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) {
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait(full_bar(s), phase, kSiteMmaFull, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = sbase + Cfg::a + s * Cfg::kABytes;
-          const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
+          const uint32_t a_addr = sbase + Cfg::ring + s * stage, b_addr = a_addr + Cfg::kABytes;
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk)
-            mma_i8(d, smem_desc_k_sw128(a_addr + 32 * kk), smem_desc_k_sw128(b_addr + 32 * kk), idesc,
-                   (g > 0 || kk > 0) ? 1u : 0u);
-          mma_commit<1>(empty_bar(s));
+            mma_i8<CG>(d, smem_desc_k_sw128(a_addr + 32 * kk), smem_desc_k_sw128(b_addr + 32 * kk), idesc,
+                       (g > 0 || kk > 0) ? 1u : 0u);
+          commit(empty_bar(s));
+          if (++s == p.stages) s = 0, phase ^= 1;
         }
-        if (ok) mma_commit<1>(tfull_bar(buf));
+        if (ok) commit(tfull_bar(buf));
       }
-      mma_commit<1>(drain_bar);
+      mma_commit<CG>(drain_bar);
       mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
     }
   } else if (warp >= kEpiWarp0) {
@@ -468,8 +518,9 @@ __global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
           if (m0 < p.M && col0 + c < p.N)
             store_chunk32<OUT_BF16>(r, p.C, p.ldc, m0, col0 + c, p.M, p.N, p.vec != 0);
         }
-        tc_fence_before();
-        mbar_arrive(tempty_bar(buf));                      // accumulator free for tile i + 2
+        tc_fence_before();                                 // accumulator free for tile i + 2
+        if constexpr (PAIR) mbar_arrive_cluster(map_shared_rank(tempty_bar(buf), 0));
+        else mbar_arrive(tempty_bar(buf));
       }
     }
   }
@@ -477,10 +528,11 @@ __global__ void __launch_bounds__(Int8Cfg::kThreads, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                                // nothing reaches into the other CTA any more
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc<1>(tmem_base, kTmemCols);
+    tmem_dealloc<CG>(tmem_base, kTmemCols);
   }
 }
 

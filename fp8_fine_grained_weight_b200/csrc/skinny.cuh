@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk) {
           if (FP8) mma_f8<1>(d, smem_desc_k_sw128(w + 32 * kk), smem_desc_k_sw128(a + 32 * kk), idesc, kk > 0);
-          else mma_i8(d, smem_desc_k_sw128(w + 32 * kk), smem_desc_k_sw128(a + 32 * kk), idesc, it > 0 || kk > 0);
+          else mma_i8<1>(d, smem_desc_k_sw128(w + 32 * kk), smem_desc_k_sw128(a + 32 * kk), idesc, it > 0 || kk > 0);
         }
         mma_commit<1>(empty_bar(s));
         if (FP8) mma_commit<1>(tfull_bar(b));

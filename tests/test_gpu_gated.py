@@ -59,7 +59,8 @@ def operands(M, N, K, pow2, seed):
 
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (2, 256, 640), (16, 128, 1152), (17, 384, 256), (64, 256, 2048),
-                                   (100, 128, 384), (127, 256, 128), (129, 640, 512), (300, 256, 1280)])
+                                   (100, 128, 384), (127, 256, 128), (129, 640, 512), (300, 256, 1280),
+                                   (513, 128, 384), (1025, 384, 128)])
 def test_forward(fq, M, N, K, pow2):
     import torch
     _, _, (qa, sa), (qw, sw) = operands(M, N, K, pow2, M + N + K)

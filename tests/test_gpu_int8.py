@@ -131,7 +131,7 @@ def check_product(C, qa, sa, qb, sb):
 
 
 SHAPES = [(1, 1, 1), (1, 16, 16), (2, 7, 33), (16, 128, 128), (17, 130, 129), (1, 7168, 2048), (64, 96, 4096),
-          (65, 2047, 300), (127, 256, 128), (128, 264, 1024), (129, 1000, 2047), (300, 513, 640), (700, 4096, 512)]
+          (65, 2047, 300), (127, 256, 128), (128, 264, 1024), (129, 1000, 2047), (300, 513, 640), (700, 4096, 512), (513, 300, 200), (1000, 2047, 129), (2500, 1100, 1300)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
