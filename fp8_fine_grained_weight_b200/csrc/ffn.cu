@@ -223,6 +223,19 @@ int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
                 : launch_int8<GATED, OUT_BF16, false>(tmA, tmB, a, sms, stream);
 }
 
+// Tensor map of a bf16 matrix read in tiles of 128 rows x 64 columns, 128-byte swizzle.
+bool encode_bf16_tiles(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int64_t ld) {
+  auto enc = tensor_map_encoder();
+  if (!enc || !bind_current_context()) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -342,19 +355,7 @@ int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int6
     return FP8Q_ERR_ALIGN;
   if (mt > 0x7FFFFFFF / (N / 128)) return FP8Q_ERR_SHAPE;     // one-dimensional grid
   CUtensorMap tmDh, tmGu;
-  auto enc = tensor_map_encoder();
-  if (!enc || !bind_current_context()) return FP8Q_ERR_CUDA;
-  auto encode = [&](CUtensorMap* tm, const void* base, int64_t cols, int64_t ld) {
-    // bf16 tiles of 128 rows x 64 columns, 128-byte swizzle
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(M)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    cuuint32_t box[2] = {64, 128};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  if (!encode(&tmDh, dH, N, lddh) || !encode(&tmGu, GU, 2 * N, ldgu)) return FP8Q_ERR_CUDA;
+  if (!encode_bf16_tiles(&tmDh, dH, M, N, lddh) || !encode_bf16_tiles(&tmGu, GU, M, 2 * N, ldgu)) return FP8Q_ERR_CUDA;
   GatedBwdArgs a{q, s, qt, st, ldq, ld_s, ldqt, ld_st, M, N};
   const auto grid = static_cast<unsigned>(mt * (N / 128));
   const auto stm = static_cast<cudaStream_t>(stream);
@@ -366,6 +367,34 @@ int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int6
     k1<<<grid, T, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
   else
     k0<<<grid, T, fp8q::kGatedBwdSmem, stm>>>(tmDh, tmGu, a);
+  return launched();
+}
+
+int fp8q_quant_act_dual_padded(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, int64_t ldq, float* s,
+                               int64_t ld_s, uint8_t* qt, int64_t ldqt, float* st, int64_t ld_st, int pow2_scale,
+                               void* stream) {
+  if (M < 0 || K < 0) return FP8Q_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8Q_OK;
+  if (!x || !q || !s || !qt || !st) return FP8Q_ERR_NULL;
+  if (K % 128 != 0 || M > 0x3FFFFFFF || K > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  const int64_t mt = (M + 127) / 128;
+  if (ldx < K || ldq < K || ld_s < M || ldqt < 128 * mt || ld_st < K) return FP8Q_ERR_SHAPE;
+  if (ldx % 8 != 0 || ldq % 8 != 0 || ldqt % 16 != 0 || !aligned(x, 16) || !aligned(q, 8) || !aligned(qt, 16) ||
+      !aligned(s, 4) || !aligned(st, 4))
+    return FP8Q_ERR_ALIGN;
+  if (mt > 0x7FFFFFFF / (K / 128)) return FP8Q_ERR_SHAPE;     // one-dimensional grid
+  CUtensorMap tmx;
+  if (!encode_bf16_tiles(&tmx, x, M, K, ldx)) return FP8Q_ERR_CUDA;
+  const auto grid = static_cast<unsigned>(mt * (K / 128));
+  const auto g32 = static_cast<uint32_t>(K / 128);
+  const auto stm = static_cast<cudaStream_t>(stream);
+  static constexpr auto k1 = fp8q::quant_act_dual_padded_kernel<true>, k0 = fp8q::quant_act_dual_padded_kernel<false>;
+  if ((pow2_scale ? resident_ctas<k1>(256, fp8q::kDualSmem) : resident_ctas<k0>(256, fp8q::kDualSmem)) <= 0)
+    return FP8Q_ERR_CUDA;
+  if (pow2_scale)
+    k1<<<grid, 256, fp8q::kDualSmem, stm>>>(tmx, M, q, ldq, s, ld_s, qt, ldqt, st, ld_st, g32);
+  else
+    k0<<<grid, 256, fp8q::kDualSmem, stm>>>(tmx, M, q, ldq, s, ld_s, qt, ldqt, st, ld_st, g32);
   return launched();
 }
 

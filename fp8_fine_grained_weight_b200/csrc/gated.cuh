@@ -416,4 +416,36 @@ __global__ void __launch_bounds__(kGatedBwdThreads, 2)
   dual_columns_pass<POW2>(lane, warp, l4, mine, m0, k0, p.qt, p.ldqt, p.st, p.ld_st);
 }
 
+// ---------------------------------------------------------------- rows and columns, any row count
+//
+// quant_act_dual_kernel for any number of rows: the tile's rows from M on read as zeros, are
+// not written to q and s, and give zero codes in qt (and scale 1 where a whole tile of a column is
+// zero), as the backward kernel above treats D.  Grid and shared memory as there.
+template <bool POW2>
+__global__ void __launch_bounds__(256, 5)
+    quant_act_dual_padded_kernel(const __grid_constant__ CUtensorMap tmx, int64_t M, uint8_t* __restrict__ q,
+                                 int64_t ldq, float* __restrict__ s, int64_t lds, uint8_t* __restrict__ qt,
+                                 int64_t ldqt, float* __restrict__ st, int64_t ldst, uint32_t G) {
+  extern __shared__ uint8_t padded_raw[];
+  const uint32_t tile = (smem_u32(padded_raw) + 1023u) & ~1023u;
+  const uint32_t bar = tile + kDualTileBytes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l4 = lane & 3;
+  const int64_t g = blockIdx.x % G, m0 = static_cast<int64_t>(blockIdx.x / G) * 128;
+  const int64_t k0 = g * 128;
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, kDualTileBytes);
+    tma_load_2d(tile, &tmx, bar, static_cast<int32_t>(k0), static_cast<int32_t>(m0));
+    tma_load_2d(tile + kDualTileBytes / 2, &tmx, bar, static_cast<int32_t>(k0 + 64), static_cast<int32_t>(m0));
+  }
+  if (!__syncthreads_and(mbar_wait(bar, 0, kSiteDual, nullptr))) return;
+  dual_rows_pass<POW2, true>(lane, warp, l4, tile, m0, M, g, k0, q, ldq, s, lds);
+  dual_columns_pass<POW2>(lane, warp, l4, tile, m0, k0, qt, ldqt, st, ldst);
+}
+
 }  // namespace fp8q

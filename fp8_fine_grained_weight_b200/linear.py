@@ -27,14 +27,19 @@ The gated layer computes H = silu(X Wg^T) * (X Wu^T) from one stacked weight W [
   Wgrad  dW [2N, K] = D^T X    A = D^T (1x128 along T),  B = X^T (1x128 along T)
 
 Any T (the products over T run on T rounded up to 128, with zero rows); K and N multiples
-of 128.
+of 128.  A step of a small layer is bound by the host, so the gated layer's function makes
+the library's calls itself on buffers carved from one allocation per direction (half the
+host time of going through the binding's functions).
 """
 from typing import Optional
 
 import torch
 
-from . import (gated_backward_quant, gemm_blockscaled, gemm_blockscaled_gated, gemm_blockscaled_ue8m0,
-               quant_act_1x128, quant_act_dual, quant_weight_128x128, transpose_blocks, workspace_bytes)
+from torch.autograd.function import once_differentiable
+
+from . import (BSCALE_BLOCK, BSCALE_ROW, OUT_BF16, _call, _on, _require_cuda, _same_device, _stream,
+               gemm_blockscaled, gemm_blockscaled_gated, gemm_blockscaled_ue8m0, quant_act_1x128,
+               quant_act_dual, quant_weight_128x128, transpose_blocks, workspace_bytes)
 
 
 def _gemm(pow2: bool):
@@ -86,53 +91,92 @@ class FP8Linear(torch.nn.Module):
         return fp8_linear(x, self.weight, self.pow2)
 
 
-def _product(qa, sa, qb, sb, pow2: bool, b_rowwise: bool = False) -> torch.Tensor:
-    """A gradient product.  The promoted GEMM's split-K workspace is this call's own: the
-    buffer cached per stream would be shared by graphs captured on that stream."""
+def _carve(device, sizes):
+    """One allocation for buffers of the given bytes: (the tensor that owns it, their offsets)."""
+    offsets, end = [], 0
+    for n in sizes:
+        offsets.append(end)
+        end += -(-n // 256) * 256
+    return torch.empty_strided((end,), (1,), dtype=torch.uint8, device=device), offsets
+
+
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """`t` contiguous and starting on 16 bytes (a view may do neither)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _pad128(n: int) -> int:
+    return -(-n // 128) * 128
+
+
+def _product(a, sa, ld_sa, b, sb, ld_sb, rowwise, out, M, N, K, pow2, ws, ws_len, stream):
+    """out [M, N] = A B^T in bf16 from raw pointers, both operands with K contiguous."""
+    mode = BSCALE_ROW if rowwise else BSCALE_BLOCK
     if pow2:
-        return gemm_blockscaled_ue8m0(qa, sa, qb, sb, out_dtype=torch.bfloat16, b_rowwise=b_rowwise)
-    with torch.cuda.device(qa.device):
-        need = workspace_bytes(qa.shape[0], qb.shape[0], qa.shape[1])
-    ws = torch.empty(need, dtype=torch.uint8, device=qa.device) if need else None
-    return gemm_blockscaled(qa, sa, qb, sb, out_dtype=torch.bfloat16, b_rowwise=b_rowwise,
-                            split_k=need > 0, workspace=ws)
+        _call("fp8_gemm_blockscaled_ue8m0", a, sa, ld_sa, b, sb, ld_sb, mode, out.data_ptr(), OUT_BF16,
+              M, N, K, K, K, N, stream)
+    else:
+        _call("fp8_gemm_blockscaled_ws", a, sa, ld_sa, b, sb, ld_sb, mode, out.data_ptr(), OUT_BF16,
+              M, N, K, K, K, N, ws, ws_len, stream)
 
 
 class FP8GatedLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> torch.Tensor:
-        T, x = x.shape[0], x.contiguous()
-        qxt = sxt = None
-        if ctx.needs_input_grad[1]:
-            if T % 128:                                    # whole 128-row tiles of X^T
-                padded = x.new_zeros((-(-T // 128) * 128, x.shape[1]))
-                padded[:T] = x
-                x = padded
-            qx, sx, qxt, sxt = quant_act_dual(x, pow2)
-            qx = qx[:T]
-        else:
-            qx, sx = quant_act_1x128(x, pow2)
-        qw, sw = quant_weight_128x128(w.contiguous(), pow2)
-        h, gu = gemm_blockscaled_gated(qx, sx, qw, sw, with_gu=True)
-        ctx.save_for_backward(gu, qxt, sxt, qw, sw)
-        ctx.pow2 = pow2
+        x, w = _packed(x), _packed(w)
+        (T, K), R = x.shape, w.shape[0]                    # R = 2N
+        N, Tp, pow2 = R // 2, _pad128(T), int(bool(pow2))
+        for_dw = ctx.needs_input_grad[1]
+        # kept for the backward pass: g and u, the codes and scales of W, those of X^T
+        kept, (gu, qw, sw, qxt, sxt) = _carve(x.device, (2 * T * R, R * K, R * K // 4096,
+                                                         K * Tp * for_dw, K * Tp // 32 * for_dw))
+        base = kept.data_ptr()
+        own, (qx, sx) = _carve(x.device, (T * K, T * K // 32))
+        q, s = own.data_ptr() + qx, own.data_ptr() + sx
+        h = torch.empty_strided((T, N), (N, 1), dtype=torch.bfloat16, device=x.device)
+        with _on(x):
+            stream = _stream(x)
+            if for_dw:
+                _call("fp8q_quant_act_dual" if T == Tp else "fp8q_quant_act_dual_padded", x.data_ptr(), T, K, K, q, K, s, T, base + qxt, Tp,
+                      base + sxt, K, pow2, stream)
+            else:
+                _call("fp8q_quant_act_1x128", x.data_ptr(), T, K, K, q, K, s, T, pow2, stream)
+            _call("fp8q_quant_weight_128x128", w.data_ptr(), R, K, K, base + qw, K, base + sw, pow2, stream)
+            _call("fp8_gemm_blockscaled_gated", q, s, T, base + qw, base + sw, h.data_ptr(), N,
+                  base + gu, R, T, N, K, K, K, stream)
+        ctx.save_for_backward(kept)
+        ctx.layout = (T, N, K, pow2, gu, qw, sw, qxt, sxt)
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh: torch.Tensor):
-        gu, qxt, sxt, qw, sw = ctx.saved_tensors
-        pow2 = ctx.pow2
-        T, K = gu.shape[0], qw.shape[1]
-        dx = dw = None
+        kept, = ctx.saved_tensors
+        T, N, K, pow2, gu, qw, sw, qxt, sxt = ctx.layout
+        for_dx, for_dw, _ = ctx.needs_input_grad
+        R, Tp, dev, base = 2 * N, _pad128(T), kept.device, kept.data_ptr()
+        dx = torch.empty_strided((T, K), (K, 1), dtype=torch.bfloat16, device=dev) if for_dx else None
+        dw = torch.empty_strided((R, K), (K, 1), dtype=torch.bfloat16, device=dev) if for_dw else None
         if T == 0:
-            return (gu.new_empty((0, K)) if ctx.needs_input_grad[0] else None,
-                    gu.new_zeros(qw.shape) if ctx.needs_input_grad[1] else None, None)
-        qd, sd, qdt, sdt = gated_backward_quant(dh.to(torch.bfloat16).contiguous(), gu, pow2)
-        if ctx.needs_input_grad[0]:
-            qwt, swt = transpose_blocks(qw, sw)
-            dx = _product(qd, sd, qwt, swt, pow2)
-        if ctx.needs_input_grad[1]:
-            dw = _product(qdt, sdt, qxt, sxt, pow2, b_rowwise=True)
+            return dx, dw.zero_() if for_dw else None, None
+        dh = _packed(dh.to(torch.bfloat16))
+        with _on(kept):
+            # The promoted GEMM's split-K workspace is this call's own: the buffer cached per stream
+            # would be shared by graphs captured on that stream.
+            ws_len = 0 if pow2 else max(workspace_bytes(T, K, R) if for_dx else 0,
+                                        workspace_bytes(R, K, Tp) if for_dw else 0)
+            own, offsets = _carve(dev, (T * R, T * R // 32, R * Tp, R * Tp // 32, K * R * for_dx,
+                                        K * R // 4096 * for_dx, ws_len))
+            qd, sd, qdt, sdt, qwt, swt, ws = (own.data_ptr() + o for o in offsets)
+            stream = _stream(kept)
+            _call("fp8q_gated_backward_quant", dh.data_ptr(), N, base + gu, R, T, N, qd, R, sd, T, qdt, Tp,
+                  sdt, R, pow2, stream)
+            if for_dx:
+                _call("fp8q_transpose_blocks", base + qw, base + sw, R, K, K, qwt, swt, R, stream)
+                _product(qd, sd, T, qwt, swt, 0, False, dx, T, K, R, pow2, ws, ws_len, stream)
+            if for_dw:
+                _product(qdt, sdt, R, base + qxt, base + sxt, K, True, dw, R, K, Tp, pow2, ws, ws_len, stream)
         return dx, dw, None
 
 
@@ -147,10 +191,15 @@ def fp8_gated_linear(x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> to
     if w.shape[1] != x.shape[1] or w.shape[0] % 256 or x.shape[1] % 128 or not w.numel():
         raise ValueError(f"w must be [2N, K] with N and K multiples of 128 and K the columns of x, got "
                          f"{tuple(w.shape)} for x {tuple(x.shape)}")
+    for t, name in ((x, "x"), (w, "w")):
+        _require_cuda(t, name)
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    _same_device(w, x.device, "w")
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
         return FP8GatedLinearFunction.apply(x, w, pow2)
-    qx, sx = quant_act_1x128(x.contiguous(), pow2)
-    qw, sw = quant_weight_128x128(w.contiguous(), pow2)
+    qx, sx = quant_act_1x128(_packed(x), pow2)
+    qw, sw = quant_weight_128x128(_packed(w), pow2)
     return gemm_blockscaled_gated(qx, sx, qw, sw)
 
 

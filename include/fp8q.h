@@ -376,6 +376,16 @@ int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int6
                               int64_t N, uint8_t* q, int64_t ldq, float* s, int64_t ld_s, uint8_t* qt,
                               int64_t ldqt, float* st, int64_t ld_st, int pow2_scale, void* stream);
 
+/*
+ * fp8q_quant_act_dual for any number of rows [Q], [P2]: (q, s) as there for the M rows, and
+ * (qt, st) the quantization of X^T with M rounded up to Mp = 128 ceil(M / 128), the columns past M
+ * zero (a tile of zeros has scale 1): E4M3 [K, Mp] (row stride ldqt bytes), fp32
+ * [Mp/128][ld_st >= K].  Equals fp8q_quant_act_dual when M % 128 == 0.  Other rules as there.
+ */
+int fp8q_quant_act_dual_padded(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, uint8_t* q,
+                               int64_t ldq, float* s, int64_t ld_s, uint8_t* qt, int64_t ldqt,
+                               float* st, int64_t ld_st, int pow2_scale, void* stream);
+
 /* Reads and clears the device error word (synchronizes `stream`).  Returns 0 when no
  * device-side error was recorded, else (site << 8) | fp8q_status. */
 int fp8q_get_device_error(void* stream);

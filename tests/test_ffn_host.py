@@ -88,6 +88,17 @@ def test_gated_backward_refusals(L):
     assert call(dH=P_MIS) == call(GU=P_MIS) == call(q=P_MIS) == call(qt=P_MIS) == call(s=P_MIS) == ALIGN
 
 
+def test_quant_act_dual_padded_refusals(L):
+    call = caller(L.fp8q_quant_act_dual_padded, x=P16, M=130, K=256, ldx=256, q=P16, ldq=256, s=P16, ld_s=130, qt=P16,
+                  ldqt=256, st=P16, ld_st=256, pow2=0, stream=NULL)
+    assert call(M=0) == OK and call(K=0) == OK
+    assert call(M=-1) == call(K=200) == call(ldx=128) == call(ldq=248) == call(ld_s=129) == call(ld_st=255) == SHAPE
+    assert call(ldqt=240) == SHAPE and call(M=1 << 30, ld_s=1 << 30, ldqt=1 << 30) == SHAPE
+    for p in ("x", "q", "s", "qt", "st"):
+        assert call(**{p: NULL}) == ENULL
+    assert call(ldx=260) == call(ldq=260) == call(ldqt=264) == call(x=P_MIS) == call(qt=P_MIS) == call(s=P_MIS) == ALIGN
+
+
 # ------------------------------------------------------------------------------- the binding
 
 @pytest.fixture
@@ -210,3 +221,13 @@ def test_gated_linear_refusals():
             fp8_gated_linear(x, w)
     with pytest.raises(TypeError, match="CUDA tensor"):
         fp8_gated_linear(ok, E(256, 128, dtype=bf16))
+
+
+def test_gated_linear_refuses_other_types(monkeypatch):
+    import fp8_fine_grained_weight_b200.linear as linear
+    monkeypatch.setattr(linear, "_require_cuda", lambda t, name: None)
+    for x, w in ((E(4, 128, dtype=f32), E(256, 128, dtype=bf16)), (E(4, 128, dtype=bf16), E(256, 128, dtype=f32))):
+        with pytest.raises(TypeError, match="bfloat16"):
+            fp8_gated_linear(x, w)
+    with pytest.raises(ValueError, match="is on"):
+        fp8_gated_linear(E(4, 128, dtype=bf16), E(256, 128, dtype=bf16).to("meta"))

@@ -236,6 +236,35 @@ def test_backward_quant_guards(fq):
         assert (b == (7.0 if b.dtype == torch.float32 else 0x5A)).all()
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("M,K", [(1, 128), (100, 256), (128, 256), (129, 384), (300, 128)])
+def test_dual_quantizer_for_any_rows(fq, M, K, pow2):
+    """Codes and scales of X and of X^T padded with zeros, bit for bit; nothing beside them."""
+    import torch
+    xb = workloads.normal_bf16(np.random.default_rng(M), (M, K), 1.0, 0.001)
+    Mp = -(-M // 128) * 128
+    x = torch.full((M, K + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x[:, :K] = to_dev_bf16(xb)
+    q = torch.full((M + 30, K + 8), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.full((K // 128, M + 5), 7.0, device="cuda")
+    qt = torch.full((K + 1, Mp + 16), 0x5A, dtype=torch.uint8, device="cuda")
+    st = torch.full((Mp // 128 + 1, K + 3), 7.0, device="cuda")
+    assert fq.lib().fp8q_quant_act_dual_padded(
+        x.data_ptr(), M, K, x.stride(0), q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0), qt.data_ptr(),
+        qt.stride(0), st.data_ptr(), st.stride(0), int(pow2), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert fq.device_error() == 0
+    padded = np.zeros((Mp, K), xb.dtype)
+    padded[:M] = xb
+    qr, sr = oracle.quant_act_1x128(xb, pow2)
+    qtr, str_ = oracle.quant_act_1x128(np.ascontiguousarray(padded.T), pow2)
+    for name, got, want in (("q", q[:M, :K], qr), ("s", s[:, :M], sr), ("qt", qt[:K, :Mp], qtr),
+                            ("st", st[:Mp // 128, :K], str_)):
+        assert_bytes_equal(name, host(got.contiguous()), want)
+        got.fill_(0x5A if got.dtype == torch.uint8 else 7.0)
+    assert all((t == (0x5A if t.dtype == torch.uint8 else 7.0)).all() for t in (q, s, qt, st))
+
+
 # --------------------------------------------------------------------------- the whole layer
 
 def layer_check(fq, T, N, K, pow2, seed):
@@ -295,6 +324,34 @@ def test_layer_needs_only_what_is_asked(fq):
     a = torch.autograd.grad(h.float().sum(), (x1, w1), retain_graph=True)
     b = torch.autograd.grad(h, (x1, w1), torch.ones_like(h))
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_layer_takes_views(fq):
+    """Operands and an upstream gradient that are transposed, sliced or off 16 bytes."""
+    import torch
+    from fp8_fine_grained_weight_b200.linear import fp8_gated_linear
+    xb, wb, _, _ = operands(70, 128, 256, False, 12)
+    x, w = to_dev_bf16(xb), to_dev_bf16(wb)
+    dh = to_dev_bf16(workloads.normal_bf16(np.random.default_rng(2), (70, 128), 1e-3))
+
+    def off(t):                                # the same values starting 2 bytes further
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        b[1:] = t.reshape(-1)
+        return b[1:].view(t.shape)
+
+    want = None
+    for f in (lambda t: t.clone(), lambda t: t.t().contiguous().t(), off):
+        x1, w1 = f(x).requires_grad_(True), f(w).requires_grad_(True)
+        h = fp8_gated_linear(x1, w1)
+        got = (h.detach(), *torch.autograd.grad(h, (x1, w1), f(dh)))
+        with torch.no_grad():
+            assert torch.equal(fp8_gated_linear(x1, w1), got[0])
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(RuntimeError):          # no second derivative
+        h = fp8_gated_linear(x1, w1)
+        g = torch.autograd.grad(h, x1, dh.clone().requires_grad_(True), create_graph=True)[0]
+        torch.autograd.grad(g.float().sum(), x1)
 
 
 def test_empty_batch(fq):
