@@ -107,16 +107,17 @@ def _call(name: str, *args) -> None:
 
 def _stream(t: torch.Tensor) -> int:
     # the handle alone: building a torch.cuda.Stream around it costs 2 us a call
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _on(t: torch.Tensor):
     """Make t's device the current one for a library call.  The library sizes grids and
     binds its driver context through the current device, so operands on another GPU must
     not be passed while a different device is current."""
-    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+    index = t.get_device()                     # -1 for CPU tensors
+    if index < 0 or index == torch._C._cuda_getDevice():
         return _NOTHING_TO_DO
-    return torch.cuda.device(t.device)
+    return torch.cuda.device(index)
 
 
 _NOTHING_TO_DO = contextlib.nullcontext()
@@ -133,7 +134,7 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: Optional[int] = None) -> None
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    if t.dim() and t.stride(-1) != 1:
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] != 1:     # of one column the stride says nothing
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
@@ -548,15 +549,16 @@ def _vector(t: torch.Tensor, name: str, n: int, device: torch.device) -> None:
 
 
 def _int8_operands(qa, sa, qb, sb):
-    """Checks of the INT8 products' operands; returns (M, rows of qb, K)."""
+    """Checks of the INT8 products' operands; returns (M, rows of qb, K, row strides of qa and qb)."""
     try:     # the checks below in one expression: a decode step's products are host-bound
         dev = qa.get_device()
         if (dev >= 0 and dev == qb.get_device() == sa.get_device() == sb.get_device()
                 and qa.dtype is qb.dtype is torch.int8 and sa.dtype is sb.dtype is torch.float32):
             (M, K), (rows, Kb), (na,), (nb,) = qa.shape, qb.shape, sa.shape, sb.shape
-            if (K == Kb and na >= M and nb >= rows and qa.stride()[1] == qb.stride()[1] == 1
-                    and sa.stride()[0] == sb.stride()[0] == 1):
-                return M, rows, K
+            (lda, ia), (ldb, ib) = qa.stride(), qb.stride()
+            if (K == Kb and na >= M and nb >= rows and ia == ib == 1
+                    and sa.is_contiguous() and sb.is_contiguous()):
+                return M, rows, K, lda, ldb
     except (AttributeError, ValueError):
         pass
     _need(qa, torch.int8, "qa", 2)
@@ -568,7 +570,7 @@ def _int8_operands(qa, sa, qb, sb):
     _same_device(qb, qa.device, "qb")
     _vector(sa, "sa", M, qa.device)
     _vector(sb, "sb", rows, qa.device)
-    return M, rows, K
+    return M, rows, K, qa.stride(0), qb.stride(0)
 
 
 def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor,
@@ -579,16 +581,16 @@ def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Te
     or fp32 [M, N].  Any M, N and K <= 131071; the rows of qa and qb start on 16 bytes
     (quant_int8_rowwise lays them out so).
     """
-    M, N, K = _int8_operands(qa, sa, qb, sb)
+    M, N, K, lda, ldb = _int8_operands(qa, sa, qb, sb)
     if out is None:
-        code = _out_code(out_dtype)
+        code, ldc = _out_code(out_dtype), N
         out = _new(M, N, out_dtype, qa.device)
     else:
-        code = _out_code(out.dtype)
+        code, ldc = _out_code(out.dtype), out.stride(0)
         _rows(out, out.dtype, "out", M, N, qa.device)
     with _on(qa):
         _call("fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
-              out.data_ptr(), code, M, N, K, qa.stride(0), qb.stride(0), out.stride(0), _stream(qa))
+              out.data_ptr(), code, M, N, K, lda, ldb, ldc, _stream(qa))
     return out
 
 
@@ -599,17 +601,18 @@ def gemm_int8_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: to
     qa int8 [M, K], sa fp32 [M]; qw int8 [2N, K] (gate rows, then up rows), sw fp32 [2N];
     h bf16 [M, N].  Sizes and alignment as ``gemm_int8``.
     """
-    M, rows, K = _int8_operands(qa, sa, qw, sw)
+    M, rows, K, lda, ldw = _int8_operands(qa, sa, qw, sw)
     if rows % 2:
         raise ValueError("qw must have an even number of rows: the gate's, then the up projection's")
     N = rows // 2
     if out is None:
-        out = _new(M, N, torch.bfloat16, qa.device)
+        ldh, out = N, _new(M, N, torch.bfloat16, qa.device)
     else:
         _rows(out, torch.bfloat16, "out", M, N, qa.device)
+        ldh = out.stride(0)
     with _on(qa):
         _call("fp8q_gemm_int8_gated", qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(),
-              out.data_ptr(), M, N, K, qa.stride(0), qw.stride(0), out.stride(0), _stream(qa))
+              out.data_ptr(), M, N, K, lda, ldw, ldh, _stream(qa))
     return out
 
 
@@ -624,23 +627,44 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
     write into.  Any M; N and K multiples of 128; FP32 or power-of-two scales.
     """
     qa, qw = _u8(qa), _u8(qw)
-    h, gu = (out if with_gu else (out, None)) if out is not None else (None, None)
-    qa, qw, _, M, rows, K = _dense_gemm_operands(qa, sa, qw, sw, False, None, torch.bfloat16, alloc=False)
+    M, rows, K, lda, ld_sa, ldw = _gated_operands(qa, sa, qw, sw)
     if rows % 256:
         raise ValueError("qw must have 2N rows with N a multiple of 128")
     N = rows // 2
+    gu, ldgu = None, 0
     if out is None:
-        h = _new(M, N, torch.bfloat16, qa.device)
-        gu = _new(M, rows, torch.bfloat16, qa.device) if with_gu else None
+        ldh, h = N, _new(M, N, torch.bfloat16, qa.device)
+        if with_gu:
+            ldgu, gu = rows, _new(M, rows, torch.bfloat16, qa.device)
     else:
+        h, gu = out if with_gu else (out, None)
         _rows(h, torch.bfloat16, "h", M, N, qa.device)
+        ldh = h.stride(0)
         if with_gu:
             _rows(gu, torch.bfloat16, "gu", M, rows, qa.device)
+            ldgu = gu.stride(0)
     with _on(qa):
-        _call("fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), sa.stride(0), qw.data_ptr(),
-              sw.data_ptr(), h.data_ptr(), h.stride(0), gu.data_ptr() if with_gu else None,
-              gu.stride(0) if with_gu else 0, M, N, K, qa.stride(0), qw.stride(0), _stream(qa))
+        _call("fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
+              h.data_ptr(), ldh, gu.data_ptr() if with_gu else None, ldgu, M, N, K, lda, ldw, _stream(qa))
     return (h, gu) if with_gu else h
+
+
+def _gated_operands(qa, sa, qw, sw):
+    """Checks of the gated FP8 product's operands; returns (M, rows of qw, K, row strides of qa, sa
+    and qw)."""
+    try:     # the checks below in one expression, as in _int8_operands
+        dev = qa.get_device()
+        if (dev >= 0 and dev == qw.get_device() == sa.get_device() == sw.get_device()
+                and qa.dtype is qw.dtype is torch.uint8 and sa.dtype is sw.dtype is torch.float32):
+            (M, K), (rows, Kw), (ga, na), sw_shape = qa.shape, qw.shape, sa.shape, sw.shape
+            (lda, ia), (ldw, iw), (ld_sa, js) = qa.stride(), qw.stride(), sa.stride()
+            if (K == Kw and ga >= K // 128 and na >= M and ia == iw == js == 1 and sw.is_contiguous()
+                    and sw_shape == (-(-rows // 128), K // 128)):
+                return M, rows, K, lda, ld_sa, ldw
+    except (AttributeError, ValueError):
+        pass
+    qa, qw, _, M, rows, K = _dense_gemm_operands(qa, sa, qw, sw, False, None, torch.bfloat16, alloc=False)
+    return M, rows, K, qa.stride(0), sa.stride(0), qw.stride(0)
 
 
 def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False, out=None):

@@ -195,6 +195,14 @@ def test_blockscaled_gated_marshalling(calls):
         fq.gemm_blockscaled_gated(qa, E(2, 4, dtype=f32), qw, sw)
 
 
+def test_one_column_needs_no_unit_stride(calls):
+    """[G, 1] scales of a single token, transposed from [1, G], keep the strides (1, G)."""
+    sa = E(1, 2, dtype=f32).t()
+    assert sa.stride() == (1, 2)
+    fq.gemm_blockscaled_gated(E(1, 256), sa, E(512, 256), E(4, 2, dtype=f32))
+    assert calls[-1][1][2] == 1
+
+
 def test_gated_backward_marshalling(calls):
     dh, gu = E(130, 128, dtype=bf16), E(130, 256, dtype=bf16)
     bufs = fq.gated_backward_quant(dh, gu)
