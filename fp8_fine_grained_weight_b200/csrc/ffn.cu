@@ -317,27 +317,27 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
   }
   GatedArgs a{};
   a.sA = sA; a.ld_sa = ld_sa; a.sW = sW;
+  a.h = static_cast<__nv_bfloat16*>(H); a.ldh = ldh;
   a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
-  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = N / Cfg::kTileN;
+  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + Cfg::kTileN - 1) / Cfg::kTileN;
   if (mt * nt > 0x7FFFFFFF || mt * nt / 148 * a.G > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
   a.mt = static_cast<int>(mt);
   a.nt = static_cast<int>(nt);
   a.n_fastest = M > 2 * N;
-  CUtensorMap tmA, tmW, tmH;
+  CUtensorMap tmA, tmW;
   if ((st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM)) != FP8Q_OK ||
-      (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kBox)) != FP8Q_OK ||
-      (st = encode_output_bf16(&tmH, H, N, M, ldh)) != FP8Q_OK)
+      (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kTileN)) != FP8Q_OK)
     return st;
   const auto s = static_cast<cudaStream_t>(stream);
   static constexpr auto plain = fp8q::gemm_fp8_gated_kernel<false>, keep = fp8q::gemm_fp8_gated_kernel<true>;
-  const int units = GU != nullptr ? resident_ctas<keep>(fp8q::kGemmThreads, Cfg::smem_bytes)
-                                  : resident_ctas<plain>(fp8q::kGemmThreads, Cfg::smem_bytes);
+  const int units = GU != nullptr ? resident_ctas<keep>(Cfg::kThreads, Cfg::smem_bytes)
+                                  : resident_ctas<plain>(Cfg::kThreads, Cfg::smem_bytes);
   if (units <= 0) return FP8Q_ERR_CUDA;
   const auto grid = static_cast<unsigned>(mt * nt < units ? mt * nt : units);
   if (GU != nullptr)
-    keep<<<grid, fp8q::kGemmThreads, Cfg::smem_bytes, s>>>(tmA, tmW, tmH, a);
+    keep<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
   else
-    plain<<<grid, fp8q::kGemmThreads, Cfg::smem_bytes, s>>>(tmA, tmW, tmH, a);
+    plain<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
   return launched();
 }
 

@@ -23,18 +23,23 @@ namespace fp8q {
 // by the group's scales and added in FP32 registers.  g and u stay in FP32 up to h; when the
 // backward pass will need them (GU) they are also stored, rounded to bf16.
 //
-// A tile is 128 rows by 128 columns of h: 256 rows of W.  They are loaded as four boxes of
-// 64 rows (gate 0-63, up 0-63, gate 64-127, up 64-127), so that the 128 accumulator columns
-// of each epilogue warpgroup are 64 gate columns and the same 64 up columns, and each thread
-// holds both factors of its 64 outputs: nothing is exchanged.  Otherwise the roles are the
-// block-scaled GEMM's: warp 0 TMA producer (3 stages of 48 KB; the fourth's room stages
-// h), warp 1 MMA issuer (one commit per group, two alternating accumulators), warp 2 scale
-// producer (slots of four groups), warps 4-11 promotion and epilogue with the register
-// split 40 / 232 (128 * 40 + 256 * 232 <= 384 * 168).
+// A tile is 128 rows by 128 columns of h: 256 rows of W, the gate's 128 and the up projection's
+// 128.  Two epilogue warpgroups each own 64 columns of h: a thread holds both factors of its 64
+// outputs, so nothing is exchanged.
+//
+//   warp 0      TMA producer: A [128 x 128 B], W [128 x 128 B] twice, 4 stages
+//   warps 1, 3  MMA issuers (N = 256), warp 1 for the even groups and accumulator 0, warp 3 for the
+//               odd ones and accumulator 1: while one's four products run, the other
+//               passes its waits (90 cycles each, even when there is nothing to wait for).
+//               One commit per group both frees the stage and publishes the partial sums.
+//   warp 2      scale producer (slots of four groups: 128 row scales, a gate and an up scale)
+//   warps 4-11  promotion and epilogue.  Registers: 128 threads * 40 + 256 * 232 <= 384 * 168.
 struct GatedArgs {
   const float* sA;      // group-major [G][ld_sa]
   int64_t ld_sa;
   const float* sW;      // [2N / 128][G]
+  __nv_bfloat16* h;     // [M, N]
+  int64_t ldh;
   __nv_bfloat16* gu;    // [M, 2N] when GU
   int64_t ld_gu, M, N;
   int G;
@@ -42,23 +47,26 @@ struct GatedArgs {
 };
 
 struct GatedCfg {
-  static constexpr int kTileM = 128, kTileN = 128, kN = 256, kStages = 3, kAccBufs = 2;
-  static constexpr int kBox = 64;                       // W rows per TMA box
+  static constexpr int kTileM = 128, kTileN = 128, kN = 2 * kTileN, kStages = 4, kAccBufs = 2;
+  static constexpr int kSets = 2, kEpiThreads = 128 * kSets, kThreads = 128 + kEpiThreads;
+  static constexpr int kSetCols = kTileN / kSets;       // columns of h per warpgroup
+  static constexpr int kRegsCtl = 40, kRegsEpi = 232;
   static constexpr uint32_t kABytes = 128 * kBK, kBBytes = kN * kBK, kStageTx = kABytes + kBBytes;
-  static constexpr int kSlotGroups = 4, kScaleSlots = 6;
-  static constexpr uint32_t kGroupFloats = 128 + 4;     // A's row scales, gate and up scale
-  static constexpr uint32_t kSlotFloats = kSlotGroups * kGroupFloats;
-  static constexpr uint32_t kOutWarpBytes = 32 * 64 * 2;   // a warp's 32 x 64 bf16 of h
+  // Scales of four groups of one tile: [128 rows][4], then the gate's and the up projection's [4].
+  static constexpr int kSlotGroups = 4, kScaleSlots = 5;
+  static constexpr uint32_t kSlotFloats = kSlotGroups * (128 + 2);
   static constexpr uint32_t a = 0;
   static constexpr uint32_t b = a + kStages * kABytes;
-  static constexpr uint32_t out = b + kStages * kBBytes;
-  static constexpr uint32_t sring = out + kEpiWarps * kOutWarpBytes;
+  static constexpr uint32_t sring = b + kStages * kBBytes;
   static constexpr uint32_t bars = sring + 4 * kScaleSlots * kSlotFloats;
-  // full[S], empty[S], tempty[2], drain, sfull[R], sempty[R]
-  static constexpr uint32_t misc = align_up(bars + 8 * (2 * kStages + kAccBufs + 1 + 2 * kScaleSlots), 16);
+  // full[S], empty[S], tempty[2], drain[2], sfull[R], sempty[R]
+  static constexpr uint32_t misc = align_up(bars + 8 * (2 * kStages + 2 * kAccBufs + 2 * kScaleSlots), 16);
   static constexpr uint32_t smem_bytes = misc + 16 + 1024;
-  static_assert(out % 1024 == 0 && kOutWarpBytes % 1024 == 0, "swizzle atoms");
-  static_assert(kStages >= kAccBufs, "a stage barrier's phase outlives the epilogue's wait for it");
+  static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0 && kTileN * kBK % 1024 == 0, "swizzle atoms");
+  static_assert(sring % 16 == 0 && kSlotFloats % 4 == 0, "float4 reads of the scales");
+  static_assert(kStages % kAccBufs == 0, "a stage barrier's phase outlives the epilogue's wait for it");
+  static_assert(kAccBufs * kN <= static_cast<int>(kTmemCols) && kSetCols == 64, "accumulators; a set's columns");
+  static_assert(128 * kRegsCtl + kEpiThreads * kRegsEpi <= kThreads * 168, "register split");
   static_assert(smem_bytes <= 232448, "fits the 227 KB opt-in shared memory");
 };
 
@@ -71,12 +79,12 @@ __device__ __forceinline__ uint4 bf16x8(const float2& a, const float2& b, const 
 }
 
 template <bool GU>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(GatedCfg::kThreads, 1)
     gemm_fp8_gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
-                          const __grid_constant__ CUtensorMap tmH, const GatedArgs p) {
+                          const GatedArgs p) {
   using Cfg = GatedCfg;
   constexpr int S = Cfg::kStages, NB = Cfg::kAccBufs, R = Cfg::kScaleSlots;
-  constexpr uint32_t SG = Cfg::kSlotGroups;
+  constexpr int SG = Cfg::kSlotGroups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -85,9 +93,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * S + NB);
-  auto sfull_bar = [&](int r) { return bar0 + 8u * (2 * S + NB + 1 + r); };
-  auto sempty_bar = [&](int r) { return bar0 + 8u * (2 * S + NB + 1 + R + r); };
+  auto drain_bar = [&](int b) { return bar0 + 8u * (2 * S + NB + b); };
+  auto sfull_bar = [&](int r) { return bar0 + 8u * (2 * S + 2 * NB + r); };
+  auto sempty_bar = [&](int r) { return bar0 + 8u * (2 * S + 2 * NB + R + r); };
   float* sring = reinterpret_cast<float*>(smem + Cfg::sring);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::misc + 4);
@@ -100,11 +108,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < NB; ++b) mbar_init(tempty_bar(b), 32 * kEpiWarps);
-    mbar_init(drain_bar, 1);
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(tempty_bar(b), Cfg::kEpiThreads / 32);   // one arrival a warp
+      mbar_init(drain_bar(b), 1);
+    }
     for (int r = 0; r < R; ++r) {
       mbar_init(sfull_bar(r), 32);                 // one cp.async arrival per producer lane
-      mbar_init(sempty_bar(r), 32 * kEpiWarps);
+      mbar_init(sempty_bar(r), Cfg::kEpiThreads / 32);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -133,7 +143,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   };
 
   if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsCtl));
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
       if (lane == 0) {
@@ -150,126 +160,127 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t b = sbase + Cfg::b + s * Cfg::kBBytes;
             tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), g * kBK, static_cast<int32_t>(row0));
             tma_load_2d(b, &tmW, full_bar(s), g * kBK, gate);
-            tma_load_2d(b + 64 * kBK, &tmW, full_bar(s), g * kBK, up);
-            tma_load_2d(b + 128 * kBK, &tmW, full_bar(s), g * kBK, gate + 64);
-            tma_load_2d(b + 192 * kBK, &tmW, full_bar(s), g * kBK, up + 64);
+            tma_load_2d(b + Cfg::kTileN * kBK, &tmW, full_bar(s), g * kBK, up);
           }
         }
         const uint32_t first = it > static_cast<uint32_t>(S) ? it - S : 0;
         for (uint32_t j = first; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 1 || warp == 3) {
+      // ---------------------------------------------------------- MMA issuers
       if (lane == 0) {
         constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, Cfg::kN);
         const uint32_t total = static_cast<uint32_t>(n_tiles) * G;
-        for (uint32_t it = 0; it < total; ++it) {
-          const int s = it % S;
-          const uint32_t buf = it % NB;
-          // the operands first (long in place), then the accumulator, which comes free just
-          // in time
-          if (!mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) break;
-          if (!mbar_wait(tempty_bar(buf), ((it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
+        const uint32_t buf = warp >> 1, d = tmem_base + buf * Cfg::kN;
+        const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
+        uint32_t s = buf, phase = 0, acc_phase = 1;        // of the full barriers; of tempty
+        for (uint32_t it = buf; it < total; it += NB) {
+          // the operands first (long in place), then the accumulator
+          if (!mbar_wait(full_bar(s), phase, kSiteMmaFull, abort_flag)) break;
+          if (!mbar_wait(tempty_bar(buf), acc_phase, kSiteMmaEmpty, abort_flag)) break;
           tc_fence_after();
-          const uint32_t a_addr = sbase + Cfg::a + s * Cfg::kABytes;
-          const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
+          const uint64_t a = a0 + s * (Cfg::kABytes >> 4), b = b0 + s * (Cfg::kBBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            mma_f8<1>(tmem_base + buf * Cfg::kN, smem_desc_k_sw128(a_addr + 32 * kk),
-                      smem_desc_k_sw128(b_addr + 32 * kk), idesc, kk > 0);
+          for (int kk = 0; kk < kBK / 32; ++kk) mma_f8<1>(d, a + 2 * kk, b + 2 * kk, idesc, kk > 0);
           mma_commit<1>(empty_bar(s));             // frees the stage and publishes the partial
+          acc_phase ^= 1;
+          s += NB;
+          if (s >= S) s -= S, phase ^= 1;
         }
-        mma_commit<1>(drain_bar);
-        mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
+        mma_commit<1>(drain_bar(buf));
+        mbar_wait(drain_bar(buf), 0, kSiteDrain, nullptr);
       }
     } else if (warp == 2) {
       // ---------------------------------------------------------- scale producer
-      uint32_t it = 0;
+      uint32_t sl = 0;
       bool ok = true;
       for (int i = 0; ok && i < n_tiles; ++i) {
         int64_t row0, col0;
         tile_at(i, row0, col0);
         const float* sW_tile = p.sW + (col0 + (lane & 1) * p.N) / 128 * G;   // lane 0 gate, 1 up
-        for (int g = 0; g < G; ++g, ++it) {
-          const uint32_t sl = it / SG;
+        for (int g0 = 0; g0 < G; g0 += SG, ++sl) {
           const int r = sl % R;
-          if (it % SG == 0 && !mbar_wait(sempty_bar(r), ((sl / R) & 1u) ^ 1u, kSiteScales, abort_flag)) {
+          if (!mbar_wait(sempty_bar(r), ((sl / R) & 1u) ^ 1u, kSiteScales, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t slot = sbase + Cfg::sring + 4u * (Cfg::kSlotFloats * r + Cfg::kGroupFloats * (it % SG));
-          const float* sa_g = p.sA + static_cast<int64_t>(g) * p.ld_sa;
+          const uint32_t slot = sbase + Cfg::sring + 4u * Cfg::kSlotFloats * r;
+          for (int k = 0; k < SG && g0 + k < G; ++k) {
+            const float* sa_g = p.sA + static_cast<int64_t>(g0 + k) * p.ld_sa;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t m = row0 + 32 * j + lane;
-            cp_async_4(slot + 4u * (32 * j + lane), sa_g + (m < p.M ? m : 0), m < p.M);
+            for (int j = 0; j < 4; ++j) {
+              const int64_t m = row0 + 32 * j + lane;
+              cp_async_4(slot + 4u * (SG * (32 * j + lane) + k), sa_g + (m < p.M ? m : 0), m < p.M);
+            }
+            if (lane < 2) cp_async_4(slot + 4u * (SG * (128 + lane) + k), sW_tile + g0 + k, true);
           }
-          if (lane < 2) cp_async_4(slot + 4u * (128 + lane), sW_tile + g, true);
-          if (it % SG == SG - 1) cp_async_arrive(sfull_bar(r));
+          cp_async_arrive(sfull_bar(r));
         }
       }
-      if (ok && it % SG != 0) cp_async_arrive(sfull_bar((it / SG) % R));   // the last, partial slot
       cp_async_wait_all();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
     // ------------------------------------------------------------ promotion + epilogue
-    const int ew = warp - kEpiWarp0;
-    const int quad = warp & 3, set = ew >> 2;
-    uint32_t acc_it = 0;
+    // With one to three warps on a scheduler every dependent instruction of this loop costs its
+    // whole latency, so it is kept short: running indices instead of divisions, one vector
+    // load for four groups' scales, one arrival per warp, one vote per wait.
+    const int quad = warp & 3, set = (warp - kEpiWarp0) >> 2;
+    const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + set * Cfg::kSetCols;
+    uint32_t s = 0, phase = 0, buf = 0, r = 0, rphase = 0;
     bool ok = true;
-    uint32_t rbuf[64];
-    float sa4[4] = {0.f, 0.f, 0.f, 0.f}, sg4[4] = {0.f, 0.f, 0.f, 0.f}, su4[4] = {0.f, 0.f, 0.f, 0.f};
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned int site) {      // warp-uniform outcome
+      if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar, parity, site, abort_flag));
+    };
     for (int i = 0; i < n_tiles; ++i) {
       float2 ag[32], au[32];                    // columns 2j, 2j + 1 of the gate's and up's 64
 #pragma unroll
       for (int j = 0; j < 32; ++j) ag[j] = au[j] = make_float2(0.0f, 0.0f);
-      for (int g = 0; g < G; ++g, ++acc_it) {
-        const uint32_t sl = acc_it / SG;
-        const int r = sl % R;
-        if (acc_it % SG == 0) {                 // a slot's four groups go to registers at once
-          if (ok) ok = mbar_wait(sfull_bar(r), (sl / R) & 1u, kSiteScales, abort_flag);
-          const int base = Cfg::kSlotFloats * r;
+      for (int g0 = 0; g0 < G; g0 += SG) {
+        wait(sfull_bar(r), rphase, kSiteScales);
+        const float4* slot = reinterpret_cast<const float4*>(sring + Cfg::kSlotFloats * r);
+        const float4 sa = slot[32 * quad + lane], sg = slot[128], su = slot[129];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty_bar(r));         // the slot is in registers
+        if (++r == R) r = 0, rphase ^= 1;
+        const float cg4[4] = {sa.x * sg.x, sa.y * sg.y, sa.z * sg.z, sa.w * sg.w};
+        const float cu4[4] = {sa.x * su.x, sa.y * su.y, sa.z * su.z, sa.w * su.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sa4[j] = sring[base + Cfg::kGroupFloats * j + quad * 32 + lane];
-            sg4[j] = sring[base + Cfg::kGroupFloats * j + 128];
-            su4[j] = sring[base + Cfg::kGroupFloats * j + 129];
+        for (int k = 0; k < SG; ++k) {
+          if (g0 + k >= G) break;
+          // the group's MMAs have completed: the commit on its stage's barrier (this wait cannot
+          // lag by a phase: group it + S needs the accumulator freed after group it + S - 2)
+          wait(empty_bar(s), phase, kSiteEpilogue);
+          if (++s == S) s = 0, phase ^= 1;
+          const uint32_t taddr = taddr0 + buf * Cfg::kN;
+          if (ok) {
+            tc_fence_after();
+            const float2 cg = make_float2(cg4[k], cg4[k]), cu = make_float2(cu4[k], cu4[k]);
+            uint32_t v[64];
+            tmem_ld_64cols(taddr, v);
+            tmem_ld_wait_regs(v);
+            promote_chunk<false>(ag, v, cg, cg, nullptr);
+            promote_chunk<false>(ag + 16, v + 32, cg, cg, nullptr);
+            tmem_ld_64cols(taddr + Cfg::kTileN, v);
+            tmem_ld_wait_regs(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));   // free for group g + 2
+            promote_chunk<false>(au, v, cu, cu, nullptr);
+            promote_chunk<false>(au + 16, v + 32, cu, cu, nullptr);
           }
-          mbar_arrive(sempty_bar(r));
-        }
-        const float2 cg = make_float2(sa4[0] * sg4[0], sa4[0] * sg4[0]);
-        const float2 cu = make_float2(sa4[0] * su4[0], sa4[0] * su4[0]);
-        sa4[0] = sa4[1]; sa4[1] = sa4[2]; sa4[2] = sa4[3];
-        sg4[0] = sg4[1]; sg4[1] = sg4[2]; sg4[2] = sg4[3];
-        su4[0] = su4[1]; su4[1] = su4[2]; su4[2] = su4[3];
-        const uint32_t buf = acc_it % NB;
-        if (ok) ok = mbar_wait(empty_bar(acc_it % S), (acc_it / S) & 1u, kSiteEpilogue, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);       // warp-uniform: TMEM loads are per warp
-        if (ok) {
-          tc_fence_after();
-          const uint32_t taddr =
-              tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * Cfg::kN + set * 128;
-          tmem_ld_64cols(taddr, rbuf);
-          tmem_ld_wait_regs(rbuf);
-          promote_chunk<false>(ag, rbuf, cg, cg, nullptr);
-          promote_chunk<false>(ag + 16, rbuf + 32, cg, cg, nullptr);
-          tmem_ld_64cols(taddr + 64, rbuf);
-          tmem_ld_wait_regs(rbuf);
-          tc_fence_before();
-          mbar_arrive(tempty_bar(buf));         // free for group g + 2
-          promote_chunk<false>(au, rbuf, cu, cu, nullptr);
-          promote_chunk<false>(au + 16, rbuf + 32, cu, cu, nullptr);
+          buf ^= 1;
         }
       }
       int64_t row0, col0;
       tile_at(i, row0, col0);
-      const int64_t m0 = row0 + 32 * quad, n0 = col0 + 64 * set;
-      if (!ok || m0 >= p.M) continue;           // warp-uniform
+      const int64_t m0 = row0 + 32 * quad, n0 = col0 + Cfg::kSetCols * set;
+      if (!ok || m0 >= p.M) continue;         // warp-uniform
+      const bool row_ok = m0 + lane < p.M;
+      uint4 v[8];
       if constexpr (GU) {
-        const bool row_ok = m0 + lane < p.M;
         uint8_t* grow = reinterpret_cast<uint8_t*>(p.gu + (m0 + lane) * p.ld_gu + n0);
-        uint4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = bf16x8(ag[4 * j], ag[4 * j + 1], ag[4 * j + 2], ag[4 * j + 3]);
         store_rows_by_quads(v, grow, row_ok);
@@ -282,26 +293,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         ag[j].x = silu_mul(ag[j].x, au[j].x);
         ag[j].y = silu_mul(ag[j].y, au[j].y);
       }
-      // h leaves through this warp's 4 KB and one TMA store (which drops rows past M): rows of
-      // 128 bytes, 16-byte chunk c of row r at c ^ (r % 8)
-      const uint32_t stg = sbase + Cfg::out + ew * Cfg::kOutWarpBytes;
-      if (lane == 0) bulk_wait_read_all();      // the previous tile's store has read it
-      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4),
-                     bf16x8(ag[4 * j], ag[4 * j + 1], ag[4 * j + 2], ag[4 * j + 3]));
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(&tmH, stg, static_cast<int32_t>(n0), static_cast<int32_t>(m0));
-        bulk_commit_group();
-      }
+      for (int j = 0; j < 8; ++j) v[j] = bf16x8(ag[4 * j], ag[4 * j + 1], ag[4 * j + 2], ag[4 * j + 3]);
+      store_rows_by_quads(v, reinterpret_cast<uint8_t*>(p.h + (m0 + lane) * p.ldh + n0), row_ok);
     }
   }
 
   // ---------------------------------------------------------------- teardown
-  if (warp >= kEpiWarp0 && lane == 0) bulk_wait_all();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
