@@ -36,6 +36,8 @@ int resident_ctas(int threads, uint32_t smem) {
   return n;
 }
 
+constexpr int64_t kMaxTiles = 0x7FFF0000;   // 32-bit tile indices, with room for a grid more
+
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
 
 constexpr int64_t kInt8MaxK = 131071;   // K 128^2 <= 2^31 - 1: the INT32 sums are exact
@@ -143,7 +145,7 @@ template <bool GATED>
 int64_t plan_skinny(SkinnyArgs* a, int mp, int sms) {
   const int cols = GATED ? 64 : 128;
   const int64_t nt = (a->N + cols - 1) / cols, units = nt * ((a->M + mp - 1) / mp);
-  if (units * 8 > 0x7FFFFFFF) return 0;
+  if (units * fp8q::kMaxSplit > kMaxTiles) return 0;
   a->nt = static_cast<int>(nt);
   a->split = skinny_split(units, a->G, sms);
   return units;
@@ -209,7 +211,7 @@ int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
   a.width = t.width;
   const int cols = GATED ? a.width / 2 : a.width, tile_m = t.pair ? 256 : 128;
   const int64_t mt = (M + tile_m - 1) / tile_m, nt = (N + cols - 1) / cols;
-  if (mt * nt > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  if (mt * nt > kMaxTiles) return FP8Q_ERR_SHAPE;
   a.mt = static_cast<int>(mt);
   a.nt = static_cast<int>(nt);
   a.n_fastest = M > rows;
@@ -320,7 +322,7 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
   a.h = static_cast<__nv_bfloat16*>(H); a.ldh = ldh;
   a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
   const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + Cfg::kTileN - 1) / Cfg::kTileN;
-  if (mt * nt > 0x7FFFFFFF || mt * nt / 148 * a.G > 0x7FFFFFFF) return FP8Q_ERR_SHAPE;
+  if (mt * nt > kMaxTiles) return FP8Q_ERR_SHAPE;
   a.mt = static_cast<int>(mt);
   a.nt = static_cast<int>(nt);
   a.n_fastest = M > 2 * N;

@@ -170,11 +170,11 @@ __global__ void __launch_bounds__(GatedCfg::kThreads, 1)
       // ---------------------------------------------------------- MMA issuers
       if (lane == 0) {
         constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, Cfg::kN);
-        const uint32_t total = static_cast<uint32_t>(n_tiles) * G;
+        const int64_t total = static_cast<int64_t>(n_tiles) * G;
         const uint32_t buf = warp >> 1, d = tmem_base + buf * Cfg::kN;
         const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
         uint32_t s = buf, phase = 0, acc_phase = 1;        // of the full barriers; of tempty
-        for (uint32_t it = buf; it < total; it += NB) {
+        for (int64_t it = buf; it < total; it += NB) {
           // the operands first (long in place), then the accumulator
           if (!mbar_wait(full_bar(s), phase, kSiteMmaFull, abort_flag)) break;
           if (!mbar_wait(tempty_bar(buf), acc_phase, kSiteMmaEmpty, abort_flag)) break;
@@ -342,7 +342,7 @@ struct GatedBwdArgs {
 // dg and du of one bf16 pair each, from words of dh, g and u.
 __device__ __forceinline__ void gated_grad_pair(uint32_t d, uint32_t& g, uint32_t& u) {
   auto one = [](float dh, float gv, float uv, float& dg, float& du) {
-    const float sg = __fdividef(1.0f, 1.0f + __expf(-gv));
+    const float sg = sigmoid(gv);
     const float ds = dh * sg;
     du = ds * gv;
     dg = ds * uv * fmaf(gv, 1.0f - sg, 1.0f);

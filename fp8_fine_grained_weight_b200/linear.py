@@ -163,9 +163,10 @@ class FP8GatedLinearFunction(torch.autograd.Function):
         dh = _packed(dh.to(torch.bfloat16))
         with _on(kept):
             # The promoted GEMM's split-K workspace is this call's own: the buffer cached per stream
-            # would be shared by graphs captured on that stream.
-            ws_len = 0 if pow2 else max(workspace_bytes(T, K, R) if for_dx else 0,
-                                        workspace_bytes(R, K, Tp) if for_dw else 0)
+            # would be shared by graphs captured on that stream.  Below 2048 a split saves less
+            # than its extra launch costs (a group of 128 takes 0.6 us, the launch 2.5 us).
+            ws_len = 0 if pow2 else max(workspace_bytes(T, K, R) if for_dx and R >= 2048 else 0,
+                                        workspace_bytes(R, K, Tp) if for_dw and Tp >= 2048 else 0)
             own, offsets = _carve(dev, (T * R, T * R // 32, R * Tp, R * Tp // 32, K * R * for_dx,
                                         K * R // 4096 * for_dx, ws_len))
             qd, sd, qdt, sdt, qwt, swt, ws = (own.data_ptr() + o for o in offsets)
@@ -174,9 +175,10 @@ class FP8GatedLinearFunction(torch.autograd.Function):
                   sdt, R, pow2, stream)
             if for_dx:
                 _call("fp8q_transpose_blocks", base + qw, base + sw, R, K, K, qwt, swt, R, stream)
-                _product(qd, sd, T, qwt, swt, 0, False, dx, T, K, R, pow2, ws, ws_len, stream)
+                _product(qd, sd, T, qwt, swt, 0, False, dx, T, K, R, pow2, ws, ws_len * (R >= 2048), stream)
             if for_dw:
-                _product(qdt, sdt, R, base + qxt, base + sxt, K, True, dw, R, K, Tp, pow2, ws, ws_len, stream)
+                _product(qdt, sdt, R, base + qxt, base + sxt, K, True, dw, R, K, Tp, pow2, ws,
+                         ws_len * (Tp >= 2048), stream)
         return dx, dw, None
 
 

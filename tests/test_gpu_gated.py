@@ -6,8 +6,8 @@ T = sum |a b|; |silu'| <= 1.1, so h is within 2e-5 (1.1 Tg |u| + |silu(g)| Tu) o
 plus the roundings of the epilogue ((8 + 2.7 |g|) 2^-23 relative, counted in the INT8 tests)
 and of bf16 (2^-8).
 
-Backward: D = [dg | du] in FP32.  With sg = 1 / (1 + exp(-g)): __expf is within
-2 + 1.173 |g| units of 2^-23, the sum, __fdividef (2 units) and each product round, so sg is
+Backward: D = [dg | du] in FP32.  With sg = 1 / (1 + exp(-g)): the exponential is within
+2 + 1.173 |g| units of 2^-23, the sum, the quotient (2 units) and each product round, so sg is
 within 5 + 1.2 |g| units relative; du adds two products: 6 + 1.2 |g|.  dg = dh u sg t with
 t = 1 + g (1 - sg): sg's error moves t by |g| sg (5 + 1.2 |g|) units absolutely and the
 subtraction and the FMA round: |g| / 2 + |t| / 2.  Then bf16 (2^-8 of the value), then E4M3

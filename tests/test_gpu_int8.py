@@ -6,11 +6,11 @@ bf16):
 
   product   acc -> FP32, times sa, times sb: 3 roundings; bf16 output one more.
   gated     g and u carry 3 FP32 roundings each.  silu(g) = g / (1 + exp(-g)): a relative
-            error d of g moves it by |1 + g (1 - sg)| d <= (1 + |g|) d; __expf is within
-            2 + floor(1.173 |g|) units of 2^-23 and enters 1 + e with weight e / (1 + e) <= 1;
-            the sum rounds once, __fdividef is within 2 units, the product with u rounds
-            once.  In units of 2^-23: 1.5 (1 + |g|) + 2 + 1.173 |g| + 0.5 + 2 + 0.5 + 1.5
-            <= 8 + 2.7 |g|.  Below g = -87.3 the quotient may be flushed: 1.2e-36 |u|.
+            error d of g moves it by |1 + g (1 - sg)| d <= (1 + |g|) d; the exponential is
+            within 2 + 1.173 |g| units of 2^-23 (as CUDA's __expf) and enters 1 + e with weight
+            e / (1 + e) <= 1; the sum rounds once, the quotient is within 2 units, the product
+            with u rounds once.  In units of 2^-23: 1.5 (1 + |g|) + 2 + 1.173 |g| + 0.5 + 2 +
+            0.5 + 1.5 <= 8 + 2.7 |g|.  Below g = -87.3 the quotient may be flushed: 1.2e-36 |u|.
 """
 import numpy as np
 import pytest
