@@ -515,6 +515,13 @@ def _new(rows: int, cols: int, dtype, device, pitch: Optional[int] = None) -> to
     return torch.empty_strided((rows, cols), (cols if pitch is None else pitch, 1), dtype=dtype, device=device)
 
 
+def _pitch(t: torch.Tensor) -> int:
+    """Row stride of a 2-D operand.  A single row's stride says nothing (a transposed column may
+    carry any): there, its columns rounded up to 16, which meets every alignment rule."""
+    rows, cols = t.shape
+    return t.stride(0) if rows != 1 else _ceil_to(cols, 16)
+
+
 def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """One scale per row: x bf16 [M, K] -> (q int8 [M, K], s fp32 [M]), x ~ q s.
 
@@ -535,7 +542,7 @@ def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.
         _rows(q, torch.int8, "q", M, K, dev)
         _vector(s, "s", M, dev)
     with _on(x):
-        _call("fp8q_quant_int8_rowwise", x.data_ptr(), M, K, x.stride(0), q.data_ptr(), q.stride(0),
+        _call("fp8q_quant_int8_rowwise", x.data_ptr(), M, K, _pitch(x), q.data_ptr(), _pitch(q),
               s.data_ptr(), _stream(x))
     return q, s
 
@@ -558,7 +565,8 @@ def _int8_operands(qa, sa, qb, sb):
             (lda, ia), (ldb, ib) = qa.stride(), qb.stride()
             if (K == Kb and na >= M and nb >= rows and ia == ib == 1
                     and sa.is_contiguous() and sb.is_contiguous()):
-                return M, rows, K, lda, ldb
+                return (M, rows, K, lda if M != 1 else _ceil_to(K, 16),
+                        ldb if rows != 1 else _ceil_to(K, 16))
     except (AttributeError, ValueError):
         pass
     _need(qa, torch.int8, "qa", 2)
@@ -570,7 +578,7 @@ def _int8_operands(qa, sa, qb, sb):
     _same_device(qb, qa.device, "qb")
     _vector(sa, "sa", M, qa.device)
     _vector(sb, "sb", rows, qa.device)
-    return M, rows, K, qa.stride(0), qb.stride(0)
+    return M, rows, K, _pitch(qa), _pitch(qb)
 
 
 def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor,
@@ -586,8 +594,9 @@ def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Te
         code, ldc = _out_code(out_dtype), N
         out = _new(M, N, out_dtype, qa.device)
     else:
-        code, ldc = _out_code(out.dtype), out.stride(0)
+        code = _out_code(out.dtype)
         _rows(out, out.dtype, "out", M, N, qa.device)
+        ldc = _pitch(out)
     with _on(qa):
         _call("fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
               out.data_ptr(), code, M, N, K, lda, ldb, ldc, _stream(qa))
@@ -609,7 +618,7 @@ def gemm_int8_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: to
         ldh, out = N, _new(M, N, torch.bfloat16, qa.device)
     else:
         _rows(out, torch.bfloat16, "out", M, N, qa.device)
-        ldh = out.stride(0)
+        ldh = _pitch(out)
     with _on(qa):
         _call("fp8q_gemm_int8_gated", qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(),
               out.data_ptr(), M, N, K, lda, ldw, ldh, _stream(qa))
@@ -639,10 +648,10 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
     else:
         h, gu = out if with_gu else (out, None)
         _rows(h, torch.bfloat16, "h", M, N, qa.device)
-        ldh = h.stride(0)
+        ldh = _pitch(h)
         if with_gu:
             _rows(gu, torch.bfloat16, "gu", M, rows, qa.device)
-            ldgu = gu.stride(0)
+            ldgu = _pitch(gu)
     with _on(qa):
         _call("fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
               h.data_ptr(), ldh, gu.data_ptr() if with_gu else None, ldgu, M, N, K, lda, ldw, _stream(qa))
@@ -660,11 +669,11 @@ def _gated_operands(qa, sa, qw, sw):
             (lda, ia), (ldw, iw), (ld_sa, js) = qa.stride(), qw.stride(), sa.stride()
             if (K == Kw and ga >= K // 128 and na >= M and ia == iw == js == 1 and sw.is_contiguous()
                     and sw_shape == (-(-rows // 128), K // 128)):
-                return M, rows, K, lda, ld_sa, ldw
+                return M, rows, K, lda if M != 1 else K, ld_sa if ga != 1 else max(ld_sa, na), ldw
     except (AttributeError, ValueError):
         pass
     qa, qw, _, M, rows, K = _dense_gemm_operands(qa, sa, qw, sw, False, None, torch.bfloat16, alloc=False)
-    return M, rows, K, qa.stride(0), sa.stride(0), qw.stride(0)
+    return M, rows, K, _pitch(qa), _pitch(sa), qw.stride(0)
 
 
 def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False, out=None):
@@ -697,9 +706,9 @@ def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False,
         _rows(st, torch.float32, "st", Mp // 128, 2 * N, dev)
     q8, qt8 = _u8(q), _u8(qt)
     with _on(dh):
-        _call("fp8q_gated_backward_quant", dh.data_ptr(), dh.stride(0), gu.data_ptr(), gu.stride(0), M, N,
-              q8.data_ptr(), q8.stride(0), s.data_ptr(), s.stride(0), qt8.data_ptr(), qt8.stride(0),
-              st.data_ptr(), st.stride(0), int(bool(pow2)), _stream(dh))
+        _call("fp8q_gated_backward_quant", dh.data_ptr(), _pitch(dh), gu.data_ptr(), _pitch(gu), M, N,
+              q8.data_ptr(), _pitch(q8), s.data_ptr(), _pitch(s), qt8.data_ptr(), qt8.stride(0),
+              st.data_ptr(), _pitch(st), int(bool(pow2)), _stream(dh))
     return q, s, qt, st
 
 

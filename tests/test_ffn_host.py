@@ -203,6 +203,24 @@ def test_one_column_needs_no_unit_stride(calls):
     assert calls[-1][1][2] == 1
 
 
+def test_a_single_rows_stride_is_not_used(calls):
+    """[1, M] scales of one K group, transposed from [M, 1], carry the row stride 1; a single row of
+    codes may carry any."""
+    sa = E(40, 1, dtype=f32).t()
+    assert sa.stride(0) == 1
+    fq.gemm_blockscaled_gated(E(40, 128), sa, E(256, 128), E(2, 1, dtype=f32))
+    assert calls[-1][1][2] >= 40
+    one = lambda n, dtype: E(n, 1, dtype=dtype).t()
+    fq.quant_int8_rowwise(one(100, bf16))
+    assert calls[-1][1][3] >= 100
+    fq.gemm_int8(one(100, i8), E(1, dtype=f32), E(3, 112, dtype=i8)[:, :100], E(3, dtype=f32), out=one(3, bf16))
+    assert calls[-1][1][9] == 112 and calls[-1][1][11] >= 3
+    fq.gemm_int8_gated(one(100, i8), E(1, dtype=f32), E(4, 112, dtype=i8)[:, :100], E(4, dtype=f32), out=one(2, bf16))
+    assert calls[-1][1][8] == 112 and calls[-1][1][10] >= 2
+    fq.gated_backward_quant(one(128, bf16), one(256, bf16))
+    assert calls[-1][1][1] >= 128 and calls[-1][1][3] >= 256
+
+
 def test_gated_backward_marshalling(calls):
     dh, gu = E(130, 128, dtype=bf16), E(130, 256, dtype=bf16)
     bufs = fq.gated_backward_quant(dh, gu)

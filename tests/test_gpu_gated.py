@@ -75,6 +75,17 @@ def test_forward(fq, M, N, K, pow2):
     assert_gemm_close("gu", host(gu), C, T, bf16=True)
 
 
+def test_forward_of_one_group_and_of_one_token(fq):
+    """Scales [1, M] and [G, 1] as a transpose leaves them, with strides that say nothing."""
+    import torch
+    for M, K in ((70, 128), (1, 384), (1, 128)):
+        _, _, (qa, sa), (qw, sw) = operands(M, 128, K, False, M + K)
+        C, T = oracle.gemm_blockscaled_ref(qa, sa, qw, sw)
+        s = to_dev(np.ascontiguousarray(sa.T)).t()
+        check_h(host(fq.gemm_blockscaled_gated(to_dev(qa), s, to_dev(qw), to_dev(sw))), C, T)
+    assert fq.device_error() == 0
+
+
 def test_forward_many_tiles(fq):
     """More tiles than SMs and both tile orders, with and without the kept g and u."""
     import torch
