@@ -16,10 +16,17 @@
 //   warp 1      TMEM owner and MMA issuer.  INT8: one accumulator over the CTA's K range.
 //               FP8: a fresh accumulator (of four) per group, promoted by the epilogue.
 //   warp 2      FP8: scale producer, MP row scales and the two weight scales per group
+//               INT8: puts the tile's row and weight scales into shared memory
 //   warp 3      idle
 //   warps 4-7   epilogue: thread t owns weight row t of the tile.  FP8: per group
 //               acc[m] += (P sW) sA[m] in FP32 registers.
 // All eight warps then sum the slices.  Two CTAs fit on an SM (about 100 KB, 128 registers).
+//
+// A decode step's product lasts a few microseconds, so what is not streaming counts (cycles of 7900
+// at 1 x 7168 x 2048 before: 1100 until the first load was issued, 1400 in a barrier that waited
+// for the outputs to be written): the first loads go out before the CTA has synchronized, the
+// scales are in shared memory before they are needed, and the last cluster barrier orders nothing
+// but the reads of the partials.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -54,8 +61,9 @@ struct SkinnyCfg {
   static constexpr int kStages = MP == 16 ? 5 : (MP == 128 ? 3 : 4);
   static constexpr int kAccBufs = KIND == kSkinnyFp8 ? 4 : 1;
   static constexpr uint32_t kAccCols = kAccBufs * MP < 32 ? 32 : kAccBufs * MP;   // a power of two
-  static constexpr int kScaleSlots = KIND == kSkinnyFp8 ? 8 : 0;
-  static constexpr uint32_t kSlotFloats = MP + 4;
+  // FP8: scales of one group per slot; INT8: one slot, the tile's row scales and 128 weight scales
+  static constexpr int kScaleSlots = KIND == kSkinnyFp8 ? 8 : 1;
+  static constexpr uint32_t kSlotFloats = KIND == kSkinnyFp8 ? MP + 4 : MP + 128;
   static constexpr uint32_t kWBytes = 128 * kBK, kABytes = MP * kBK, kStageTx = kWBytes + kABytes;
   static constexpr uint32_t w = 0;
   static constexpr uint32_t a = w + kStages * kWBytes;
@@ -131,6 +139,16 @@ __global__ void __launch_bounds__(256, 2)
   const int g0 = static_cast<int>(static_cast<int64_t>(p.G) * rank / p.split);
   const int n_g = static_cast<int>(static_cast<int64_t>(p.G) * (rank + 1) / p.split) - g0;   // >= 1
 
+  auto load_stage = [&](int it) {
+    const int s = it % S;
+    mbar_arrive_expect_tx(full_bar(s), Cfg::kStageTx);
+    const uint32_t w = sbase + Cfg::w + s * Cfg::kWBytes;
+    const int32_t x = (g0 + it) * kBK;
+    tma_load_2d(w, &tmW, full_bar(s), x, static_cast<int32_t>(col0));
+    if (GATED) tma_load_2d(w + 64 * kBK, &tmW, full_bar(s), x, static_cast<int32_t>(p.N + col0));
+    tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), x, static_cast<int32_t>(row0));
+  };
+  const int n_first = n_g < S ? n_g : S;                   // stages that wait for nothing
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
@@ -147,10 +165,7 @@ __global__ void __launch_bounds__(256, 2)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmW);
+    for (int it = 0; it < n_first; ++it) load_stage(it);
   }
   if (warp == 1) {
     tmem_alloc<1>(smem_u32(tmem_slot), Cfg::kAccCols);
@@ -164,16 +179,10 @@ __global__ void __launch_bounds__(256, 2)
   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int it = 0;
+      int it = n_first;
       for (; it < n_g; ++it) {
-        const int s = it % S;
-        if (!mbar_wait(empty_bar(s), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) break;
-        mbar_arrive_expect_tx(full_bar(s), Cfg::kStageTx);
-        const uint32_t w = sbase + Cfg::w + s * Cfg::kWBytes;
-        const int32_t x = (g0 + it) * kBK;
-        tma_load_2d(w, &tmW, full_bar(s), x, static_cast<int32_t>(col0));
-        if (GATED) tma_load_2d(w + 64 * kBK, &tmW, full_bar(s), x, static_cast<int32_t>(p.N + col0));
-        tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), x, static_cast<int32_t>(row0));
+        if (!mbar_wait(empty_bar(it % S), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) break;
+        load_stage(it);
       }
       // every issued load lands before the ring is reused (bounded; loads end on their own)
       for (int j = it > S ? it - S : 0; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
@@ -207,8 +216,8 @@ __global__ void __launch_bounds__(256, 2)
     // -------------------------------------------------------------- scale producer
     const float* sW = p.sB + (col0 + (lane & 1) * p.N) / 128 * p.G;        // lane 0 gate, 1 up
     for (int it = 0; it < n_g; ++it) {
-      const int r = it % (R ? R : 1);
-      if (!mbar_wait(sempty_bar(r), ((it / (R ? R : 1)) & 1u) ^ 1u, kSiteScales, abort_flag)) break;
+      const int r = it % R;
+      if (!mbar_wait(sempty_bar(r), ((it / R) & 1u) ^ 1u, kSiteScales, abort_flag)) break;
       const uint32_t slot = sbase + Cfg::sring + 4u * Cfg::kSlotFloats * r;
       const float* sa = p.sA + static_cast<int64_t>(g0 + it) * p.ld_sa;
 #pragma unroll
@@ -220,6 +229,14 @@ __global__ void __launch_bounds__(256, 2)
       cp_async_arrive(sfull_bar(r));
     }
     cp_async_wait_all();
+  } else if (!FP8 && warp == 2) {
+    // read after the cluster barrier below
+    for (int m = lane; m < MP; m += 32) sring[m] = row0 + m < p.M ? __ldg(p.sA + row0 + m) : 0.0f;
+    for (int c = lane; c < 128; c += 32) {
+      const bool up = c >= kCols;                          // GATED: 64 gate scales, 64 up scales
+      const int64_t n = col0 + (up ? c - kCols : c);
+      sring[MP + c] = n < p.N ? __ldg(p.sB + (up ? p.N : 0) + n) : 0.0f;
+    }
   }
 
   // The CTA's partials, [m][weight row].  The ring is free to hold them: the last group's
@@ -235,8 +252,8 @@ __global__ void __launch_bounds__(256, 2)
       for (int j = 0; j < MP / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
       bool ok = true;
       for (int it = 0; it < n_g; ++it) {
-        const int r = it % (R ? R : 1), b = it % NB;
-        if (ok) ok = mbar_wait(sfull_bar(r), (it / (R ? R : 1)) & 1u, kSiteScales, abort_flag);
+        const int r = it % R, b = it % NB;
+        if (ok) ok = mbar_wait(sfull_bar(r), (it / R) & 1u, kSiteScales, abort_flag);
         if (ok) ok = mbar_wait(tfull_bar(b), (it / NB) & 1u, kSiteEpilogue, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
@@ -320,11 +337,11 @@ __global__ void __launch_bounds__(256, 2)
     total(m, c, v);
     if constexpr (GATED) total(m, 64 + c, u);
     if constexpr (!FP8) {
-      const float sa = __ldg(p.sA + row);
+      const float sa = sring[m];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j < left) v[j] = (v[j] * sa) * __ldg(p.sB + n + j);
-        if (GATED && j < left) u[j] = (u[j] * sa) * __ldg(p.sB + p.N + n + j);
+        v[j] = (v[j] * sa) * sring[MP + c + j];
+        if (GATED) u[j] = (u[j] * sa) * sring[MP + 64 + c + j];
       }
     }
     if constexpr (GATED) {
@@ -359,8 +376,10 @@ __global__ void __launch_bounds__(256, 2)
   }
 
   // ---------------------------------------------------------------- teardown
+  // The partials stay until all have read them (each read has been used: nothing to order).
   __syncwarp();
-  cluster_sync();                                          // the partials stay until all have read
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem_base, Cfg::kAccCols);
