@@ -155,7 +155,7 @@ def check_codes(D, e, q, s, pow2):
     amax_lo = lo.reshape(R, Cn // 128, 128).max(2) / 448 * (1 - 2.0 ** -23)
     amax_hi = hi.reshape(R, Cn // 128, 128).max(2) / 448 * (1 + 2.0 ** -23)
     st = s.T
-    zero = amax_hi < 1e-37
+    zero = (amax_hi < 1e-37) | ((amax_lo <= 0) & (st == 1))     # a tile that may be all zeros
     if pow2:
         ok = (st >= amax_lo) & (st < 2 * amax_hi)
         assert (np.frexp(st)[0] == 0.5).all()
