@@ -34,6 +34,11 @@ namespace fp8q {
 //               One commit per group both frees the stage and publishes the partial sums.
 //   warp 2      scale producer (slots of four groups: 128 row scales, a gate and an up scale)
 //   warps 4-11  promotion and epilogue.  Registers: 128 threads * 40 + 256 * 232 <= 384 * 168.
+//
+// Measured: 228 us at 8192 x 2048 x 7168 (0.63 of the FP8 peak), 33 us at 1024 rows.  The promotion
+// loop bounds it (tensor pipe 55 % busy): about 900 cycles per group against 512 of MMAs, of
+// which the 64 packed FMAs per thread are 260.  Three warpgroups on 96 columns (277 us) and four
+// at 112 registers (250 us) measured slower; one issuer and per-thread arrivals 233 us.
 struct GatedArgs {
   const float* sA;      // group-major [G][ld_sa]
   int64_t ld_sa;
@@ -322,6 +327,9 @@ __global__ void __launch_bounds__(GatedCfg::kThreads, 1)
 // h and 4 written, against 6 + 4 + 4 + 4 for an elementwise pass followed by the quantizer.
 // Rows past M read as zeros, so qt and st cover M rounded up to 128 rows (zero codes,
 // which add nothing to dW).
+//
+// Measured: 44 us (power-of-two scales) at 8192 x 2048, 0.58 of HBM; it issues 61 % of the time.
+// With 256 threads per block, each quantizing both halves in turn, it took 50 us.
 //
 // Grid: one block of 512 threads per 128 x 128 tile of h, columns fastest, two to an SM.  The
 // three bf16 input tiles come by TMA (two boxes of 64 columns each); dg replaces g and du

@@ -20,6 +20,10 @@
 //   warp 3      idle
 //   warps 4-7   epilogue: thread t owns weight row t of the tile.  FP8: per group
 //               acc[m] += (P sW) sA[m] in FP32 registers.
+// Measured: INT8 1 x 7168 x 2048 in 7.0 us, 64 x 7168 x 7168 in 14.2 us (8 us of streaming at the
+// HBM rate, 2 of launch, the rest joining the sums); FP8 gated 16 x 2048 x 7168 in 10.7 us.  The
+// wide kernels take 9-10, 24 and 34 us.
+//
 // All eight warps then sum the slices.  Two CTAs fit on an SM (about 100 KB, 128 registers).
 //
 // A decode step's product lasts a few microseconds, so what is not streaming counts (cycles of 7900
