@@ -100,7 +100,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _call(name: str, *args) -> None:
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != 0:
         raise Fp8qError(name, st)
 
@@ -121,6 +121,16 @@ def _on(t: torch.Tensor):
 
 
 _NOTHING_TO_DO = contextlib.nullcontext()
+
+
+def _launch(t: torch.Tensor, name: str, *args) -> None:
+    """A library call on t's device and its current stream (the call's last argument)."""
+    index = t.get_device()
+    if index < 0 or index == torch._C._cuda_getDevice():
+        _call(name, *args, _stream(t))
+    else:
+        with torch.cuda.device(index):
+            _call(name, *args, _stream(t))
 
 
 def _require_cuda(t: torch.Tensor, name: str) -> None:
@@ -535,15 +545,15 @@ def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.
         raise ValueError("x must have at least one column")
     dev = x.device
     if out is None:
-        q = _new(M, K, torch.int8, dev, _ceil_to(K, 16))
+        ldq = _ceil_to(K, 16)
+        q = _new(M, K, torch.int8, dev, ldq)
         s = torch.empty_strided((M,), (1,), dtype=torch.float32, device=dev)
     else:
         q, s = out
         _rows(q, torch.int8, "q", M, K, dev)
         _vector(s, "s", M, dev)
-    with _on(x):
-        _call("fp8q_quant_int8_rowwise", x.data_ptr(), M, K, _pitch(x), q.data_ptr(), _pitch(q),
-              s.data_ptr(), _stream(x))
+        ldq = _pitch(q)
+    _launch(x, "fp8q_quant_int8_rowwise", x.data_ptr(), M, K, _pitch(x), q.data_ptr(), ldq, s.data_ptr())
     return q, s
 
 
@@ -597,9 +607,8 @@ def gemm_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Te
         code = _out_code(out.dtype)
         _rows(out, out.dtype, "out", M, N, qa.device)
         ldc = _pitch(out)
-    with _on(qa):
-        _call("fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
-              out.data_ptr(), code, M, N, K, lda, ldb, ldc, _stream(qa))
+    _launch(qa, "fp8q_gemm_int8", qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
+            out.data_ptr(), code, M, N, K, lda, ldb, ldc)
     return out
 
 
@@ -619,9 +628,8 @@ def gemm_int8_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: to
     else:
         _rows(out, torch.bfloat16, "out", M, N, qa.device)
         ldh = _pitch(out)
-    with _on(qa):
-        _call("fp8q_gemm_int8_gated", qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(),
-              out.data_ptr(), M, N, K, lda, ldw, ldh, _stream(qa))
+    _launch(qa, "fp8q_gemm_int8_gated", qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(),
+            out.data_ptr(), M, N, K, lda, ldw, ldh)
     return out
 
 
@@ -652,9 +660,8 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
         if with_gu:
             _rows(gu, torch.bfloat16, "gu", M, rows, qa.device)
             ldgu = _pitch(gu)
-    with _on(qa):
-        _call("fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
-              h.data_ptr(), ldh, gu.data_ptr() if with_gu else None, ldgu, M, N, K, lda, ldw, _stream(qa))
+    _launch(qa, "fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
+            h.data_ptr(), ldh, gu.data_ptr() if with_gu else None, ldgu, M, N, K, lda, ldw)
     return (h, gu) if with_gu else h
 
 
@@ -705,10 +712,9 @@ def gated_backward_quant(dh: torch.Tensor, gu: torch.Tensor, pow2: bool = False,
         _rows(_u8(qt), torch.uint8, "qt", 2 * N, Mp, dev)
         _rows(st, torch.float32, "st", Mp // 128, 2 * N, dev)
     q8, qt8 = _u8(q), _u8(qt)
-    with _on(dh):
-        _call("fp8q_gated_backward_quant", dh.data_ptr(), _pitch(dh), gu.data_ptr(), _pitch(gu), M, N,
-              q8.data_ptr(), _pitch(q8), s.data_ptr(), _pitch(s), qt8.data_ptr(), qt8.stride(0),
-              st.data_ptr(), _pitch(st), int(bool(pow2)), _stream(dh))
+    _launch(dh, "fp8q_gated_backward_quant", dh.data_ptr(), _pitch(dh), gu.data_ptr(), _pitch(gu), M, N,
+            q8.data_ptr(), _pitch(q8), s.data_ptr(), _pitch(s), qt8.data_ptr(), qt8.stride(0),
+            st.data_ptr(), _pitch(st), int(bool(pow2)))
     return q, s, qt, st
 
 
