@@ -40,6 +40,25 @@ constexpr int64_t kMaxTiles = 0x7FFF0000;   // 32-bit tile indices, with room fo
 
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
 
+template <typename... Params>
+int launch_clusters(void (*kern)(Params...), int64_t grid, int cluster, int threads, uint32_t smem,
+                    cudaStream_t stream, const Params&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return FP8Q_OK;
+  (void)cudaGetLastError();   // reported here, not by the next launch check
+  return FP8Q_ERR_CUDA;
+}
+
 constexpr int64_t kInt8MaxK = 131071;   // K 128^2 <= 2^31 - 1: the INT32 sums are exact
 
 int check_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB, const void* C, int out_dtype,
@@ -89,18 +108,7 @@ int launch_skinny(const CUtensorMap& tmA, const CUtensorMap& tmW, const SkinnyAr
   using Cfg = fp8q::SkinnyCfg<KIND, MP>;
   static constexpr auto kern = fp8q::gemm_skinny_kernel<KIND, GATED, OUT_BF16, MP>;
   if (resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes) <= 0) return FP8Q_ERR_CUDA;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(a.split);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * a.split));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::smem_bytes;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmA, tmW, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  return launch_clusters(kern, units * a.split, a.split, Cfg::kThreads, Cfg::smem_bytes, stream, tmA, tmW, a);
 }
 
 // Rows of A per tile: the smallest that holds M, or the largest.
@@ -182,18 +190,7 @@ int launch_int8(const CUtensorMap& tmA, const CUtensorMap& tmB, Int8Args a, int 
   const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt;
   constexpr int cg = PAIR ? 2 : 1;
   const int64_t units = tiles < sms / cg ? tiles : sms / cg;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cg;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * cg));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::smem_bytes;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  return launch_clusters(kern, units * cg, cg, Cfg::kThreads, Cfg::smem_bytes, stream, tmA, tmB, a);
 }
 
 template <bool GATED, bool OUT_BF16>

@@ -123,6 +123,39 @@ def test_product_path_requires_cuda_tensors():
         fq.gated_backward_quant(E(4, 128, dtype=bf16), E(4, 256, dtype=bf16))
 
 
+def test_calls_run_on_the_operands_device(calls, monkeypatch):
+    """On a device that is not the current one, the library call is made inside that device's
+    context; on the current one, without a switch."""
+    entered = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *a):
+            entered.append(None)
+
+    class On(torch.Tensor):
+        def get_device(self):
+            return 3
+
+    t = E(4, 128, dtype=bf16).as_subclass(On)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(fq, "_call", lambda name, *args: entered.append(name))
+    fq._launch(t, "a")
+    with fq._on(t):
+        entered.append("b")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3)
+    fq._launch(t, "c")
+    with fq._on(t):
+        entered.append("d")
+    assert entered == [3, "a", None, 3, "b", None, "c", "d"]
+
+
 def test_quant_int8_marshalling(calls):
     q, s = fq.quant_int8_rowwise(E(5, 100, dtype=bf16))
     assert q.shape == (5, 100) and q.stride() == (112, 1) and s.shape == (5,)
