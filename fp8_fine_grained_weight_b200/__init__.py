@@ -68,6 +68,9 @@ SIGNATURES = {
                                          _i64, _vp, _i64, _i32, _vp]),
     "fp8q_quant_act_dual_padded": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                                           _vp, _i64, _i32, _vp]),
+    "fp8q_gated_linear_sizes": (_i32, [_i64, _i64, _i64, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]),
+    "fp8q_gated_linear_forward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "fp8q_gated_linear_backward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
     "fp8q_get_device_error": (_i32, [_vp]),
     "fp8q_selftest_wait_timeout": (_i32, [ctypes.c_uint64, _vp]),
     "fp8q_status_string": (ctypes.c_char_p, [_i32]),

@@ -222,6 +222,59 @@ int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
                 : launch_int8<GATED, OUT_BF16, false>(tmA, tmB, a, sms, stream);
 }
 
+// Buffers of the gated layer, as byte offsets into what the forward pass keeps and into the
+// scratch of either direction (each on 256 bytes).
+struct GatedLayer {
+  int64_t Tp;                                        // T rounded up to 128
+  size_t gu, qw, sw, qxt, sxt, kept;                 // kept: g and u; W's codes and scales; X^T's
+  size_t qx, sx, forward;                            // forward scratch: X's codes and scales
+  size_t qd, sd, qdt, sdt, qwt, swt, ws, ws_bytes, backward;   // backward: D's, D^T's, W^T's; split-K
+};
+
+int gated_layer(GatedLayer* l, int64_t T, int64_t N, int64_t K, bool for_dx, bool for_dw, bool pow2) {
+  if (T < 0 || N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return FP8Q_ERR_SHAPE;
+  if (T > 0x3FFFFFFF || N > 0x1FFFFFFF || K > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  const int64_t R = 2 * N, Tp = (T + 127) / 128 * 128;
+  l->Tp = Tp;
+  size_t end = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = end;
+    end += (static_cast<size_t>(bytes) + 255) / 256 * 256;
+    return at;
+  };
+  l->gu = take(2 * T * R);
+  l->qw = take(R * K);
+  l->sw = take(R / 128 * (K / 128) * 4);
+  l->qxt = take(for_dw ? K * Tp : 0);
+  l->sxt = take(for_dw ? Tp / 128 * K * 4 : 0);
+  l->kept = end;
+  end = 0;
+  l->qx = take(T * K);
+  l->sx = take(K / 128 * T * 4);
+  l->forward = end;
+  end = 0;
+  l->qd = take(T * R);
+  l->sd = take(R / 128 * T * 4);
+  l->qdt = take(R * Tp);
+  l->sdt = take(Tp / 128 * R * 4);
+  l->qwt = take(for_dx ? K * R : 0);
+  l->swt = take(for_dx ? K / 128 * (R / 128) * 4 : 0);
+  // The promoted products may split their last wave along K.  Below 2048 a split saves less than
+  // its extra launch costs (a group of 128 takes 0.6 us, the launch 2.5 us).
+  l->ws_bytes = 0;
+  if (!pow2 && T > 0) {
+    size_t dx = 0, dw = 0;
+    int st = FP8Q_OK;
+    if (for_dx && R >= 2048) st = fp8_gemm_workspace_size(T, K, R, &dx);
+    if (st == FP8Q_OK && for_dw && Tp >= 2048) st = fp8_gemm_workspace_size(R, K, Tp, &dw);
+    if (st != FP8Q_OK) return st;
+    l->ws_bytes = std::max(dx, dw);
+  }
+  l->ws = take(static_cast<int64_t>(l->ws_bytes));
+  l->backward = end;
+  return FP8Q_OK;
+}
+
 // Tensor map of a bf16 matrix read in tiles of 128 rows x 64 columns, 128-byte swizzle.
 bool encode_bf16_tiles(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int64_t ld) {
   auto enc = tensor_map_encoder();
@@ -395,6 +448,74 @@ int fp8q_quant_act_dual_padded(const void* x, int64_t M, int64_t K, int64_t ldx,
   else
     k0<<<grid, 256, fp8q::kDualSmem, stm>>>(tmx, M, q, ldq, s, ld_s, qt, ldqt, st, ld_st, g32);
   return launched();
+}
+
+int fp8q_gated_linear_sizes(int64_t T, int64_t N, int64_t K, int for_dx, int for_dw, int pow2_scale,
+                            size_t* bytes) {
+  if (!bytes) return FP8Q_ERR_NULL;
+  GatedLayer l{};
+  const int st = gated_layer(&l, T, N, K, for_dx != 0, for_dw != 0, pow2_scale != 0);
+  bytes[0] = l.kept;
+  bytes[1] = l.forward;
+  bytes[2] = l.backward;
+  return st;
+}
+
+int fp8q_gated_linear_forward(const void* x, const void* w, int64_t T, int64_t N, int64_t K, int for_dw,
+                              int pow2_scale, void* kept, void* scratch, void* H, void* stream) {
+  GatedLayer l{};
+  int st = gated_layer(&l, T, N, K, false, for_dw != 0, true);   // (no split-K on the way forward)
+  if (st != FP8Q_OK) return st;
+  if (!w || !kept || (T > 0 && (!x || !scratch || !H))) return FP8Q_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(kept, 16) || !aligned(scratch, 16) || !aligned(H, 16))
+    return FP8Q_ERR_ALIGN;
+  auto* k8 = static_cast<uint8_t*>(kept);
+  auto* s8 = static_cast<uint8_t*>(scratch);
+  auto f32 = [](uint8_t* p) { return reinterpret_cast<float*>(p); };
+  const int64_t R = 2 * N;
+  if ((st = fp8q_quant_weight_128x128(w, R, K, K, k8 + l.qw, K, f32(k8 + l.sw), pow2_scale, stream)) != FP8Q_OK || T == 0)
+    return st;
+  if (!for_dw)
+    st = fp8q_quant_act_1x128(x, T, K, K, s8 + l.qx, K, f32(s8 + l.sx), T, pow2_scale, stream);
+  else
+    st = (l.Tp == T ? fp8q_quant_act_dual : fp8q_quant_act_dual_padded)(
+        x, T, K, K, s8 + l.qx, K, f32(s8 + l.sx), T, k8 + l.qxt, l.Tp, f32(k8 + l.sxt), K, pow2_scale, stream);
+  if (st != FP8Q_OK) return st;
+  return fp8_gemm_blockscaled_gated(s8 + l.qx, f32(s8 + l.sx), T, k8 + l.qw, f32(k8 + l.sw), H, N, k8 + l.gu, R, T, N,
+                                    K, K, K, stream);
+}
+
+int fp8q_gated_linear_backward(const void* dH, const void* kept, int64_t T, int64_t N, int64_t K, int for_dw,
+                               int pow2_scale, void* scratch, void* dX, void* dW, void* stream) {
+  GatedLayer l{};
+  int st = gated_layer(&l, T, N, K, dX != nullptr, for_dw != 0, pow2_scale != 0);
+  if (st != FP8Q_OK) return st;
+  if (T == 0) return FP8Q_OK;
+  if (!dH || !kept || !scratch || (dW && !for_dw)) return FP8Q_ERR_NULL;
+  if (!aligned(dH, 16) || !aligned(kept, 16) || !aligned(scratch, 16) || !aligned(dX, 16) || !aligned(dW, 16))
+    return FP8Q_ERR_ALIGN;
+  const auto* k8 = static_cast<const uint8_t*>(kept);
+  auto* s8 = static_cast<uint8_t*>(scratch);
+  auto f32 = [](const uint8_t* p) { return reinterpret_cast<float*>(const_cast<uint8_t*>(p)); };
+  const int64_t R = 2 * N, Tp = l.Tp;
+  st = fp8q_gated_backward_quant(dH, N, k8 + l.gu, R, T, N, s8 + l.qd, R, f32(s8 + l.sd), T, s8 + l.qdt, Tp,
+                                 f32(s8 + l.sdt), R, pow2_scale, stream);
+  auto product = [&](const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* B, const float* sB, int64_t ld_sb,
+                     int mode, void* C, int64_t m, int64_t n, int64_t k) {
+    if (pow2_scale)
+      return fp8_gemm_blockscaled_ue8m0(A, sA, ld_sa, B, sB, ld_sb, mode, C, FP8Q_OUT_BF16, m, n, k, k, k, n, stream);
+    const bool split = k >= 2048 && l.ws_bytes > 0;
+    return fp8_gemm_blockscaled_ws(A, sA, ld_sa, B, sB, ld_sb, mode, C, FP8Q_OUT_BF16, m, n, k, k, k, n,
+                                   split ? s8 + l.ws : nullptr, split ? l.ws_bytes : 0, stream);
+  };
+  if (st == FP8Q_OK && dX) {
+    st = fp8q_transpose_blocks(k8 + l.qw, f32(k8 + l.sw), R, K, K, s8 + l.qwt, f32(s8 + l.swt), R, stream);
+    if (st == FP8Q_OK)
+      st = product(s8 + l.qd, f32(s8 + l.sd), T, s8 + l.qwt, f32(s8 + l.swt), 0, FP8Q_BSCALE_BLOCK128x128, dX, T, K, R);
+  }
+  if (st == FP8Q_OK && dW)
+    st = product(s8 + l.qdt, f32(s8 + l.sdt), R, k8 + l.qxt, f32(k8 + l.sxt), K, FP8Q_BSCALE_ROW1x128, dW, R, K, Tp);
+  return st;
 }
 
 }  // extern "C"

@@ -27,19 +27,20 @@ The gated layer computes H = silu(X Wg^T) * (X Wu^T) from one stacked weight W [
   Wgrad  dW [2N, K] = D^T X    A = D^T (1x128 along T),  B = X^T (1x128 along T)
 
 Any T (the products over T run on T rounded up to 128, with zero rows); K and N multiples
-of 128.  A step of a small layer is bound by the host, so the gated layer's function makes
-the library's calls itself on buffers carved from one allocation per direction (half the
-host time of going through the binding's functions).
+of 128.  A step of a small layer is bound by the host, so each direction is one call of the
+library.
 """
+import ctypes
+import functools
 from typing import Optional
 
 import torch
 
 from torch.autograd.function import once_differentiable
 
-from . import (BSCALE_BLOCK, BSCALE_ROW, OUT_BF16, _call, _on, _require_cuda, _same_device, _stream,
-               gemm_blockscaled, gemm_blockscaled_gated, gemm_blockscaled_ue8m0, quant_act_1x128,
-               quant_act_dual, quant_weight_128x128, transpose_blocks, workspace_bytes)
+from . import (_call, _launch, _require_cuda, _same_device, gemm_blockscaled, gemm_blockscaled_gated,
+               gemm_blockscaled_ue8m0, quant_act_1x128, quant_act_dual, quant_weight_128x128,
+               transpose_blocks)
 
 
 def _gemm(pow2: bool):
@@ -91,94 +92,59 @@ class FP8Linear(torch.nn.Module):
         return fp8_linear(x, self.weight, self.pow2)
 
 
-def _carve(device, sizes):
-    """One allocation for buffers of the given bytes: (the tensor that owns it, their offsets)."""
-    offsets, end = [], 0
-    for n in sizes:
-        offsets.append(end)
-        end += -(-n // 256) * 256
-    return torch.empty_strided((end,), (1,), dtype=torch.uint8, device=device), offsets
-
-
 def _packed(t: torch.Tensor) -> torch.Tensor:
     """`t` contiguous and starting on 16 bytes (a view may do neither)."""
     t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
 
 
-def _pad128(n: int) -> int:
-    return -(-n // 128) * 128
+def _new(device, dtype, *shape) -> torch.Tensor:
+    strides = (1,) if len(shape) == 1 else (shape[1], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def _product(a, sa, ld_sa, b, sb, ld_sb, rowwise, out, M, N, K, pow2, ws, ws_len, stream):
-    """out [M, N] = A B^T in bf16 from raw pointers, both operands with K contiguous."""
-    mode = BSCALE_ROW if rowwise else BSCALE_BLOCK
-    if pow2:
-        _call("fp8_gemm_blockscaled_ue8m0", a, sa, ld_sa, b, sb, ld_sb, mode, out.data_ptr(), OUT_BF16,
-              M, N, K, K, K, N, stream)
-    else:
-        _call("fp8_gemm_blockscaled_ws", a, sa, ld_sa, b, sb, ld_sb, mode, out.data_ptr(), OUT_BF16,
-              M, N, K, K, K, N, ws, ws_len, stream)
+@functools.lru_cache(maxsize=1024)
+def _gated_bytes(device: int, T: int, N: int, K: int, for_dx: bool, for_dw: bool, pow2: bool):
+    """Bytes that the layer keeps, of its forward scratch and of its backward scratch."""
+    out = (ctypes.c_size_t * 3)()
+    with torch.cuda.device(device):
+        _call("fp8q_gated_linear_sizes", T, N, K, for_dx, for_dw, pow2, out)
+    return tuple(out)
 
 
 class FP8GatedLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> torch.Tensor:
-        x, w = _packed(x), _packed(w)
-        (T, K), R = x.shape, w.shape[0]                    # R = 2N
-        N, Tp, pow2 = R // 2, _pad128(T), int(bool(pow2))
-        for_dw = ctx.needs_input_grad[1]
-        # kept for the backward pass: g and u, the codes and scales of W, those of X^T
-        kept, (gu, qw, sw, qxt, sxt) = _carve(x.device, (2 * T * R, R * K, R * K // 4096,
-                                                         K * Tp * for_dw, K * Tp // 32 * for_dw))
-        base = kept.data_ptr()
-        own, (qx, sx) = _carve(x.device, (T * K, T * K // 32))
-        q, s = own.data_ptr() + qx, own.data_ptr() + sx
-        h = torch.empty_strided((T, N), (N, 1), dtype=torch.bfloat16, device=x.device)
-        with _on(x):
-            stream = _stream(x)
-            if for_dw:
-                _call("fp8q_quant_act_dual" if T == Tp else "fp8q_quant_act_dual_padded", x.data_ptr(), T, K, K, q, K, s, T, base + qxt, Tp,
-                      base + sxt, K, pow2, stream)
-            else:
-                _call("fp8q_quant_act_1x128", x.data_ptr(), T, K, K, q, K, s, T, pow2, stream)
-            _call("fp8q_quant_weight_128x128", w.data_ptr(), R, K, K, base + qw, K, base + sw, pow2, stream)
-            _call("fp8_gemm_blockscaled_gated", q, s, T, base + qw, base + sw, h.data_ptr(), N,
-                  base + gu, R, T, N, K, K, K, stream)
+        x, w, pow2 = _packed(x), _packed(w), bool(pow2)
+        (T, K), N, dev = x.shape, w.shape[0] // 2, x.device
+        for_dx, for_dw, _ = ctx.needs_input_grad
+        kept_bytes, scratch_bytes, ctx.scratch = _gated_bytes(dev.index, T, N, K, for_dx, for_dw, pow2)
+        kept = _new(dev, torch.uint8, kept_bytes)          # g and u, the codes of W and of X^T
+        scratch = _new(dev, torch.uint8, scratch_bytes)
+        h = _new(dev, torch.bfloat16, T, N)
+        _launch(x, "fp8q_gated_linear_forward", x.data_ptr(), w.data_ptr(), T, N, K, for_dw, pow2,
+                kept.data_ptr(), scratch.data_ptr(), h.data_ptr())
         ctx.save_for_backward(kept)
-        ctx.layout = (T, N, K, pow2, gu, qw, sw, qxt, sxt)
+        ctx.sizes = (T, N, K, for_dw, pow2)
         return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh: torch.Tensor):
         kept, = ctx.saved_tensors
-        T, N, K, pow2, gu, qw, sw, qxt, sxt = ctx.layout
+        T, N, K, kept_for_dw, pow2 = ctx.sizes
         for_dx, for_dw, _ = ctx.needs_input_grad
-        R, Tp, dev, base = 2 * N, _pad128(T), kept.device, kept.data_ptr()
-        dx = torch.empty_strided((T, K), (K, 1), dtype=torch.bfloat16, device=dev) if for_dx else None
-        dw = torch.empty_strided((R, K), (K, 1), dtype=torch.bfloat16, device=dev) if for_dw else None
+        dev = kept.device
+        dx = _new(dev, torch.bfloat16, T, K) if for_dx else None
+        dw = _new(dev, torch.bfloat16, 2 * N, K) if for_dw else None
         if T == 0:
             return dx, dw.zero_() if for_dw else None, None
         dh = _packed(dh.to(torch.bfloat16))
-        with _on(kept):
-            # The promoted GEMM's split-K workspace is this call's own: the buffer cached per stream
-            # would be shared by graphs captured on that stream.  Below 2048 a split saves less
-            # than its extra launch costs (a group of 128 takes 0.6 us, the launch 2.5 us).
-            ws_len = 0 if pow2 else max(workspace_bytes(T, K, R) if for_dx and R >= 2048 else 0,
-                                        workspace_bytes(R, K, Tp) if for_dw and Tp >= 2048 else 0)
-            own, offsets = _carve(dev, (T * R, T * R // 32, R * Tp, R * Tp // 32, K * R * for_dx,
-                                        K * R // 4096 * for_dx, ws_len))
-            qd, sd, qdt, sdt, qwt, swt, ws = (own.data_ptr() + o for o in offsets)
-            stream = _stream(kept)
-            _call("fp8q_gated_backward_quant", dh.data_ptr(), N, base + gu, R, T, N, qd, R, sd, T, qdt, Tp,
-                  sdt, R, pow2, stream)
-            if for_dx:
-                _call("fp8q_transpose_blocks", base + qw, base + sw, R, K, K, qwt, swt, R, stream)
-                _product(qd, sd, T, qwt, swt, 0, False, dx, T, K, R, pow2, ws, ws_len * (R >= 2048), stream)
-            if for_dw:
-                _product(qdt, sdt, R, base + qxt, base + sxt, K, True, dw, R, K, Tp, pow2, ws,
-                         ws_len * (Tp >= 2048), stream)
+        # one buffer of this call's own, the split-K workspace in it: the one cached per stream would
+        # be shared by graphs captured on that stream
+        scratch = _new(dev, torch.uint8, ctx.scratch)
+        _launch(kept, "fp8q_gated_linear_backward", dh.data_ptr(), kept.data_ptr(), T, N, K, kept_for_dw, pow2,
+                scratch.data_ptr(), dx.data_ptr() if for_dx else None, dw.data_ptr() if for_dw else None)
         return dx, dw, None
 
 

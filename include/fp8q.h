@@ -386,6 +386,32 @@ int fp8q_quant_act_dual_padded(const void* x_bf16, int64_t M, int64_t K, int64_t
                                int64_t ldq, float* s, int64_t ld_s, uint8_t* qt, int64_t ldqt,
                                float* st, int64_t ld_st, int pow2_scale, void* stream);
 
+/*
+ * The gated layer H = silu(X Wg^T) * (X Wu^T) with its gradients, composed of the calls above
+ * (each direction one call, so that a small step is not bound by the host).  W [2N, K] holds the
+ * gate's N rows and then the up projection's; X, W, H, dH, dX, dW are bf16 and contiguous.
+ *
+ * fp8q_gated_linear_sizes fills in the device bytes to provide: bytes[0] kept from the forward to the
+ * backward call, bytes[1] forward scratch, bytes[2] backward scratch (for the gradients asked for;
+ * it depends on the current device).  for_dw says whether dW will be asked for: it has to be the
+ * same in all three calls.
+ *
+ * forward   quantizes X (1x128; with for_dw also X^T) and W (128x128), H by
+ *           fp8_gemm_blockscaled_gated; keeps g, u, the codes of W and of X^T
+ * backward  fp8q_gated_backward_quant, then dX = D W (K = 2N) unless dX is NULL, and
+ *           dW = D^T X (K = T rounded up to 128) unless dW is NULL, by the block-scaled GEMMs
+ *           (power-of-two scales: fp8_gemm_blockscaled_ue8m0)
+ * Any T; N and K multiples of 128; every pointer on 16 bytes.  T == 0: forward quantizes W only,
+ * backward does nothing (dW is not written).
+ */
+int fp8q_gated_linear_sizes(int64_t T, int64_t N, int64_t K, int for_dx, int for_dw, int pow2_scale,
+                            size_t* bytes);
+int fp8q_gated_linear_forward(const void* x, const void* w, int64_t T, int64_t N, int64_t K, int for_dw,
+                              int pow2_scale, void* kept, void* scratch, void* H, void* stream);
+int fp8q_gated_linear_backward(const void* dH, const void* kept, int64_t T, int64_t N, int64_t K,
+                               int for_dw, int pow2_scale, void* scratch, void* dX, void* dW,
+                               void* stream);
+
 /* Reads and clears the device error word (synchronizes `stream`).  Returns 0 when no
  * device-side error was recorded, else (site << 8) | fp8q_status. */
 int fp8q_get_device_error(void* stream);

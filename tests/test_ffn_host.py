@@ -99,6 +99,44 @@ def test_quant_act_dual_padded_refusals(L):
     assert call(ldx=260) == call(ldq=260) == call(ldqt=264) == call(x=P_MIS) == call(qt=P_MIS) == call(s=P_MIS) == ALIGN
 
 
+def sizes(L, *args):
+    out = (ctypes.c_size_t * 3)()
+    assert L.fp8q_gated_linear_sizes(*args, out) == OK
+    return list(out)
+
+
+def test_gated_linear_sizes_and_refusals(L):
+    """Every buffer of the layer is inside the bytes that it asks for: kept holds g, u (bf16), W's
+    codes and scales and X^T's; the scratches the codes and scales of X, and of D, D^T and W^T."""
+    up = lambda *n: sum(-(-b // 256) * 256 for b in n)
+    for T, N, K in ((1, 128, 128), (200, 256, 384), (256, 384, 640)):
+        R, Tp = 2 * N, -(-T // 128) * 128
+        w = (R * K, R * K // 4096)
+        d = (T * R, T * R // 32, R * Tp, R * Tp // 32)
+        assert sizes(L, T, N, K, 1, 1, 1) == [up(2 * T * R, *w, K * Tp, K * Tp // 32), up(T * K, T * K // 32),
+                                              up(*d, K * R, K * R // 4096)]
+        assert sizes(L, T, N, K, 0, 1, 0)[2] == up(*d)            # (no split-K below 2048)
+        assert sizes(L, T, N, K, 1, 0, 0)[0] == up(2 * T * R, *w)
+    out = (ctypes.c_size_t * 3)()
+    for T, N, K in ((-1, 128, 128), (4, 100, 128), (4, 128, 100), (4, 0, 128), (4, 128, 0), (4, 1 << 30, 128)):
+        assert L.fp8q_gated_linear_sizes(T, N, K, 1, 1, 1, out) == SHAPE
+    assert L.fp8q_gated_linear_sizes(4, 128, 128, 1, 1, 1, None) == ENULL
+    call = caller(L.fp8q_gated_linear_forward, x=P16, w=P16, T=4, N=128, K=128, for_dw=1, pow2=0, kept=P16, scratch=P16,
+                  H=P16, stream=NULL)
+    assert call(N=100) == call(K=100) == call(T=-1) == SHAPE
+    for p in ("x", "w", "kept", "scratch", "H"):
+        assert call(**{p: NULL}) == ENULL and call(**{p: P_MIS}) == ALIGN
+    call = caller(L.fp8q_gated_linear_backward, dH=P16, kept=P16, T=4, N=128, K=128, for_dw=1, pow2=1, scratch=P16, dX=P16,
+                  dW=P16, stream=NULL)
+    assert call(T=0) == OK
+    assert call(N=100) == call(K=100) == call(T=-1) == SHAPE
+    for p in ("dH", "kept", "scratch"):
+        assert call(**{p: NULL}) == ENULL
+    for p in ("dH", "kept", "scratch", "dX", "dW"):
+        assert call(**{p: P_MIS}) == ALIGN
+    assert call(for_dw=0) == ENULL                                # dW without what it needs
+
+
 # ------------------------------------------------------------------------------- the binding
 
 @pytest.fixture
