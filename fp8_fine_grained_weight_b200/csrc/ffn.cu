@@ -76,9 +76,8 @@ int check_int8(const int8_t* A, const float* sA, const int8_t* B, const float* s
 
 // Tiling of the wide INT8 kernel: CTA pairs or single CTAs, and columns of B per tile, by the
 // least time over all waves.  A tile's time per 128 K-elements, in ns, fitted to measurements
-// with K = 7168: single CTAs 296 / 293 / 313 / 305 / 350 / 374 / 384 for widths 64, 96, 128, 160,
-// 192, 224 and 256 (up to 64 bytes a cycle from L2), pairs 305 / 304 / 304 / 309 / 320 / 350 /
-// 355.  Below a width of 160 the four dependent products of a stage, 70 ns each, set the time.
+// with 4096 x 7168 x 7168: single CTAs 204 / 229 / 300 / 360 for widths 64, 128, 192 and 256 (up to
+// 64 bytes a cycle from L2), pairs 207 / 221 / 264 / 330.
 struct Int8Tiling {
   bool pair;
   int width;
@@ -93,7 +92,7 @@ Int8Tiling int8_tiling(int64_t M, int64_t rows, bool gated, int sms) {
     const int units = pair ? sms / 2 : sms;
     for (int w = 256; w >= step; w -= step) {
       const int64_t waves = (mt * ((rows + w - 1) / w) + units - 1) / units;
-      const int64_t cost = waves * (pair ? std::max(30500, 21500 + 54 * w) : std::max(29600, 21000 + 68 * w));
+      const int64_t cost = waves * (pair ? std::max(20700, 11000 + 86 * w) : std::max(20400, 9500 + 105 * w));
       if (cost < best_cost) best = {pair != 0, w}, best_cost = cost;
     }
   }

@@ -151,50 +151,58 @@ __global__ void __launch_bounds__(GatedCfg::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsCtl));
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
-      if (lane == 0) {
-        uint32_t it = 0;
-        bool ok = true;
-        for (int i = 0; ok && i < n_tiles; ++i) {
-          int64_t row0, col0;
-          tile_at(i, row0, col0);
-          const int32_t gate = static_cast<int32_t>(col0), up = static_cast<int32_t>(p.N + col0);
-          for (int g = 0; g < G; ++g, ++it) {
-            const int s = it % S;
-            if (!mbar_wait(empty_bar(s), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) { ok = false; break; }
+      const bool leader = elect_one();
+      uint32_t it = 0, s = 0, phase = 1;                   // of the empty barriers
+      bool ok = true;
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        int64_t row0, col0;
+        tile_at(i, row0, col0);
+        const int32_t row = static_cast<int32_t>(row0);
+        const int32_t gate = static_cast<int32_t>(col0), up = static_cast<int32_t>(p.N + col0);
+        for (int g = 0; g < G; ++g, ++it) {
+          if (!mbar_wait_warp(empty_bar(s), phase, kSiteProducer, abort_flag)) { ok = false; break; }
+          const uint32_t a = sbase + Cfg::a + s * Cfg::kABytes, b = sbase + Cfg::b + s * Cfg::kBBytes;
+          if (leader) {
             mbar_arrive_expect_tx(full_bar(s), Cfg::kStageTx);
-            const uint32_t b = sbase + Cfg::b + s * Cfg::kBBytes;
-            tma_load_2d(sbase + Cfg::a + s * Cfg::kABytes, &tmA, full_bar(s), g * kBK, static_cast<int32_t>(row0));
+            tma_load_2d(a, &tmA, full_bar(s), g * kBK, row);
             tma_load_2d(b, &tmW, full_bar(s), g * kBK, gate);
             tma_load_2d(b + Cfg::kTileN * kBK, &tmW, full_bar(s), g * kBK, up);
           }
+          if (++s == S) s = 0, phase ^= 1;
         }
-        const uint32_t first = it > static_cast<uint32_t>(S) ? it - S : 0;
-        for (uint32_t j = first; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
       }
+      // every issued load lands before the CTA can exit (bounded; loads end on their own)
+      for (uint32_t j = it > S ? it - S : 0; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
+      __syncwarp();
     } else if (warp == 1 || warp == 3) {
       // ---------------------------------------------------------- MMA issuers
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, Cfg::kN);
-        const int64_t total = static_cast<int64_t>(n_tiles) * G;
-        const uint32_t buf = warp >> 1, d = tmem_base + buf * Cfg::kN;
-        const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
-        uint32_t s = buf, phase = 0, acc_phase = 1;        // of the full barriers; of tempty
-        for (int64_t it = buf; it < total; it += NB) {
-          // the operands first (long in place), then the accumulator
-          if (!mbar_wait(full_bar(s), phase, kSiteMmaFull, abort_flag)) break;
-          if (!mbar_wait(tempty_bar(buf), acc_phase, kSiteMmaEmpty, abort_flag)) break;
-          tc_fence_after();
-          const uint64_t a = a0 + s * (Cfg::kABytes >> 4), b = b0 + s * (Cfg::kBBytes >> 4);
+      // (whole warps with one lane issuing, so that the operands are in uniform registers)
+      constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, Cfg::kN);
+      const int64_t total = static_cast<int64_t>(n_tiles) * G;
+      const uint32_t buf = warp >> 1, d = tmem_base + buf * Cfg::kN;
+      const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
+      const bool leader = elect_one();
+      uint32_t s = buf, phase = 0, acc_phase = 1;          // of the full barriers; of tempty
+      for (int64_t it = buf; it < total; it += NB) {
+        // the operands first (long in place), then the accumulator
+        if (!mbar_wait_warp(full_bar(s), phase, kSiteMmaFull, abort_flag)) break;
+        if (!mbar_wait_warp(tempty_bar(buf), acc_phase, kSiteMmaEmpty, abort_flag)) break;
+        tc_fence_after();
+        const uint64_t a = a0 + s * (Cfg::kABytes >> 4), b = b0 + s * (Cfg::kBBytes >> 4);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk) mma_f8<1>(d, a + 2 * kk, b + 2 * kk, idesc, kk > 0);
           mma_commit<1>(empty_bar(s));             // frees the stage and publishes the partial
-          acc_phase ^= 1;
-          s += NB;
-          if (s >= S) s -= S, phase ^= 1;
         }
+        acc_phase ^= 1;
+        s += NB;
+        if (s >= S) s -= S, phase ^= 1;
+      }
+      if (leader) {
         mma_commit<1>(drain_bar(buf));
         mbar_wait(drain_bar(buf), 0, kSiteDrain, nullptr);
       }
+      __syncwarp();
     } else if (warp == 2) {
       // ---------------------------------------------------------- scale producer
       uint32_t sl = 0;

@@ -241,6 +241,19 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
+// Wait for a phase by a whole warp; the outcome is warp-uniform (and known to be to the compiler).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, unsigned int site, volatile int* abort) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, site, abort));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // 1 / (1 + exp(-g)) by the hardware's base-2 exponential and reciprocal: exp within 2 + 0.75 |g|
 // units of 2^-23 (2^-22 for ex2, the rounding of g log2(e) and of the constant), the sum rounded
 // once, the reciprocal within one unit.  For g < -87.3 the divisor passes 2^126 and the result is
@@ -406,49 +419,57 @@ __global__ void __launch_bounds__(Int8Cfg<PAIR>::kThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint32_t stage = Cfg::stage_bytes(p.width);
-      uint32_t it = 0, phase = 1;                          // of the empty barriers
-      int s = 0;
-      bool ok = true;
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        int64_t row0, col0;
-        tile_at(i, row0, col0);
-        for (int g = 0; g < G; ++g, ++it) {
-          if (!mbar_wait(empty_bar(s), phase, kSiteProducer, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a_addr = sbase + Cfg::ring + s * stage, b_addr = a_addr + Cfg::kABytes;
-          const int32_t x = g * kBK, ya = static_cast<int32_t>(row0), yb = static_cast<int32_t>(col0);
+    const uint32_t stage = Cfg::stage_bytes(p.width);
+    const bool leader = elect_one();
+    uint32_t it = 0, phase = 1;                            // of the empty barriers
+    int s = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      int64_t row0, col0;
+      tile_at(i, row0, col0);
+      const int32_t ya = static_cast<int32_t>(row0), yb = static_cast<int32_t>(col0);
+      const int32_t yu = static_cast<int32_t>(GATED ? p.N + col0 : col0 + p.width / 2);   // the other half of B
+      for (int g = 0; g < G; ++g, ++it) {
+        if (!mbar_wait_warp(empty_bar(s), phase, kSiteProducer, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a_addr = sbase + Cfg::ring + s * stage, b_addr = a_addr + Cfg::kABytes;
+        const int32_t x = g * kBK;
+        if (leader) {
           if constexpr (PAIR) {
             // both CTAs' bytes count on rank 0's barrier, whose phase its own arrival opens
             if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * stage);
             const uint32_t bar = map_shared_rank(full_bar(s), 0);
             tma_load_2d_pair(a_addr, &tmA, bar, x, ya);
-            tma_load_2d_pair(b_addr, &tmB, bar, x,
-                             rank == 0 ? yb : static_cast<int32_t>(GATED ? p.N + col0 : col0 + p.width / 2));
+            tma_load_2d_pair(b_addr, &tmB, bar, x, rank == 0 ? yb : yu);
           } else {
             mbar_arrive_expect_tx(full_bar(s), stage);
             tma_load_2d(a_addr, &tmA, full_bar(s), x, ya);
             tma_load_2d(b_addr, &tmB, full_bar(s), x, yb);
-            if (GATED) tma_load_2d(b_addr + cols * kBK, &tmB, full_bar(s), x, static_cast<int32_t>(p.N + col0));
+            if (GATED) tma_load_2d(b_addr + cols * kBK, &tmB, full_bar(s), x, yu);
           }
-          if (++s == p.stages) s = 0, phase ^= 1;
         }
+        if (++s == p.stages) s = 0, phase ^= 1;
       }
-      // Every issued load lands before the CTA can exit: rank 0 sees its stages' bytes arrive, rank
-      // 1 sees their products, which waited for them, complete (bounded; loads end on their
-      // own).
-      const uint32_t n = p.stages;
-      for (uint32_t j = it > n ? it - n : 0; j < it; ++j)
-        mbar_wait(rank == 0 ? full_bar(j % n) : empty_bar(j % n), (j / n) & 1u, kSiteDrain, nullptr);
     }
+    // Every issued load lands before the CTA can exit: rank 0 sees its stages' bytes arrive, rank
+    // 1 sees their products, which waited for them, complete (bounded; loads end on their
+    // own).
+    const uint32_t n = p.stages;
+    for (uint32_t j = it > n ? it - n : 0; j < it; ++j)
+      mbar_wait(rank == 0 ? full_bar(j % n) : empty_bar(j % n), (j / n) & 1u, kSiteDrain, nullptr);
+    __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the loop and one lane issues, so that descriptors and addresses live in
+    // uniform registers: from a lane's own registers each MMA takes 64 cycles to issue and a
+    // group 560 in all, more than its 512 cycles of products.
+    if (rank == 0) {
       const uint32_t idesc = idesc_s8_s32(Cfg::kTileM, p.width);
       const uint32_t stage = Cfg::stage_bytes(p.width);
+      const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::ring);
+      const bool leader = elect_one();
       auto commit = [&](uint32_t bar) {
         if constexpr (PAIR) mma_commit_pair(bar, 3);
         else mma_commit<1>(bar);
@@ -458,26 +479,29 @@ __global__ void __launch_bounds__(Int8Cfg<PAIR>::kThreads, 1)
       bool ok = true;
       for (int i = 0; ok && i < n_tiles; ++i) {
         const uint32_t buf = i & 1;
-        if (!mbar_wait(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
+        if (!mbar_wait_warp(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
         const uint32_t d = tmem_base + buf * Cfg::kMaxWidth;
         for (int g = 0; g < G; ++g) {
-          if (!mbar_wait(full_bar(s), phase, kSiteMmaFull, abort_flag)) {
+          if (!mbar_wait_warp(full_bar(s), phase, kSiteMmaFull, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = sbase + Cfg::ring + s * stage, b_addr = a_addr + Cfg::kABytes;
+          const uint64_t a = a0 + s * (stage >> 4), b = a + (Cfg::kABytes >> 4);
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            mma_i8<CG>(d, smem_desc_k_sw128(a_addr + 32 * kk), smem_desc_k_sw128(b_addr + 32 * kk), idesc,
-                       (g > 0 || kk > 0) ? 1u : 0u);
-          commit(empty_bar(s));
+            for (int kk = 0; kk < kBK / 32; ++kk) mma_i8<CG>(d, a + 2 * kk, b + 2 * kk, idesc, (g > 0 || kk > 0) ? 1u : 0u);
+            commit(empty_bar(s));
+          }
           if (++s == p.stages) s = 0, phase ^= 1;
         }
-        if (ok) commit(tfull_bar(buf));
+        if (ok && leader) commit(tfull_bar(buf));
       }
-      mma_commit<CG>(drain_bar);
-      mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
+      if (leader) {
+        mma_commit<CG>(drain_bar);
+        mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
+      }
+      __syncwarp();
     }
   } else if (warp >= kEpiWarp0) {
     // -------------------------------------------------------------- epilogue

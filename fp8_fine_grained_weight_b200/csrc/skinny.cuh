@@ -182,36 +182,42 @@ __global__ void __launch_bounds__(256, 2)
 
   if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int it = n_first;
-      for (; it < n_g; ++it) {
-        if (!mbar_wait(empty_bar(it % S), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) break;
-        load_stage(it);
-      }
-      // every issued load lands before the ring is reused (bounded; loads end on their own)
-      for (int j = it > S ? it - S : 0; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
+    // (here and in the issuer: whole warps with one lane issuing, so that the operands are in
+    // uniform registers)
+    __syncwarp();
+    const bool leader = elect_one();
+    int it = n_first;
+    for (; it < n_g; ++it) {
+      if (!mbar_wait_warp(empty_bar(it % S), ((it / S) & 1u) ^ 1u, kSiteProducer, abort_flag)) break;
+      if (leader) load_stage(it);
     }
+    // every issued load lands before the ring is reused (bounded; loads end on their own)
+    for (int j = it > S ? it - S : 0; j < it; ++j) mbar_wait(full_bar(j % S), (j / S) & 1u, kSiteDrain, nullptr);
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, MP) : idesc_s8_s32(128, MP);
-      bool ok = true;
-      for (int it = 0; it < n_g; ++it) {
-        const int s = it % S, b = it % NB;
-        ok = mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag);
-        if (ok && FP8) ok = mbar_wait(tempty_bar(b), ((it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t w = sbase + Cfg::w + s * Cfg::kWBytes, a = sbase + Cfg::a + s * Cfg::kABytes;
-        const uint32_t d = tmem_base + b * MP;
+    constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, MP) : idesc_s8_s32(128, MP);
+    const uint64_t w0 = smem_desc_k_sw128(sbase + Cfg::w), a0 = smem_desc_k_sw128(sbase + Cfg::a);
+    const bool leader = elect_one();
+    bool ok = true;
+    for (int it = 0; it < n_g; ++it) {
+      const int s = it % S, b = it % NB;
+      ok = mbar_wait_warp(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag);
+      if (ok && FP8) ok = mbar_wait_warp(tempty_bar(b), ((it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t w = w0 + s * (Cfg::kWBytes >> 4), a = a0 + s * (Cfg::kABytes >> 4);
+      const uint32_t d = tmem_base + b * MP;
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk) {
-          if (FP8) mma_f8<1>(d, smem_desc_k_sw128(w + 32 * kk), smem_desc_k_sw128(a + 32 * kk), idesc, kk > 0);
-          else mma_i8<1>(d, smem_desc_k_sw128(w + 32 * kk), smem_desc_k_sw128(a + 32 * kk), idesc, it > 0 || kk > 0);
+          if (FP8) mma_f8<1>(d, w + 2 * kk, a + 2 * kk, idesc, kk > 0);
+          else mma_i8<1>(d, w + 2 * kk, a + 2 * kk, idesc, it > 0 || kk > 0);
         }
         mma_commit<1>(empty_bar(s));
         if (FP8) mma_commit<1>(tfull_bar(b));
       }
+    }
+    if (leader) {
       if (!FP8 && ok) mma_commit<1>(tfull_bar(0));
       mma_commit<1>(drain_bar);
       mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
