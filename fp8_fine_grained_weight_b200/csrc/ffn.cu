@@ -137,14 +137,21 @@ int sm_count() {
   return n;
 }
 
-// Whether the few-row kernel takes the product: always up to its largest tile of rows, and beyond
-// that, up to 512 rows, while the wide kernel's 128 x 256 tiles would leave most SMs idle.
-// (us, few-row / wide.  INT8 N 7168 K 7168: 128 rows 17.5 / 23.0, 256 22.5 / 24.5, 512 34.5 /
-// 27.6.  INT8 gated N 2048 K 7168: 256 rows 16.5 / 22.2, 512 20.5 / 23.7, 1000 32.8 / 28.7.
-// FP8 gated N 2048 K 7168: 64 rows 12.3 / 34, 256 22.3 / 34.0, 512 37.2 / 34.0.)
-bool few_rows(int64_t M, int64_t rows, int sms, bool fp8) {
-  if (M <= (fp8 ? 64 : 128)) return true;
-  return M <= 512 && (M + 127) / 128 * ((rows + 255) / 256) * (fp8 ? 3 : 2) <= sms;
+// Whether the few-row kernel takes the product: always up to 64 rows, and up to 512 while the wide
+// kernel would leave most SMs idle (INT8: its 128 x 128 tiles half of them, and beyond 128 rows K
+// has to be long enough to be split; FP8: its 128 x 256 tiles three quarters).
+// us, few-row / wide:
+//   INT8 N 7168 K 7168        128 rows 16.2 / 17.5, 192 19.6 / 16.8, 256 20.9 / 17.4
+//   INT8 N 28672 K 2048       64 rows 17.0 / 16.6, 128 20.5 / 17.0
+//   INT8 N 2048 K 1496        128 rows 6.7 / 7.1, 256 8.0 / 7.3;   N 512 K 7168, 512 rows 10.1 / 15.1
+//   INT8 gated N 2048 K 7168  128 rows 12.4 / 15.7, 256 15.6 / 15.8, 384 17.7 / 16.7
+//   FP8 gated N 2048 K 7168   64 rows 11.5 / 30.8, 256 22.2 / 31.4, 384 37.2 / 31.5
+bool few_rows(int64_t M, int64_t rows, int64_t G, int sms, bool fp8) {
+  if (M <= 64) return true;
+  if (M > 512) return false;
+  const int64_t mt = (M + 127) / 128;
+  if (fp8) return mt * ((rows + 255) / 256) * 4 <= sms;
+  return mt * ((rows + 127) / 128) * 2 <= sms && (M <= 128 || G >= 32);
 }
 
 // Fills in the tiling of the few-row kernel; returns its tile count, or 0 on failure.
@@ -198,7 +205,7 @@ int run_int8(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
   const int sms = sm_count();
   if (sms <= 0) return FP8Q_ERR_CUDA;
   const int64_t rows = GATED ? 2 * N : N;
-  if (few_rows(M, rows, sms, false))
+  if (few_rows(M, rows, (K + 127) / 128, sms, false))
     return run_int8_skinny<GATED, OUT_BF16>(A, sA, B, sB, C, M, N, K, lda, ldb, ldc, sms, stream);
   const Int8Tiling t = int8_tiling(M, rows, GATED, sms);
   Int8Args a{};
@@ -346,7 +353,7 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
   }
   const int sms = sm_count();
   if (sms <= 0) return FP8Q_ERR_CUDA;
-  if (few_rows(M, 2 * N, sms, true)) {
+  if (few_rows(M, 2 * N, K / 128, sms, true)) {
     constexpr int KIND = fp8q::kSkinnyFp8;
     const int mp = skinny_rows(M, 64);
     SkinnyArgs a{};
