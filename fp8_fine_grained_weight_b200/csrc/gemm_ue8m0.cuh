@@ -231,54 +231,61 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      uint32_t it = 0, sc = 0;     // groups and scale slots issued so far
-      bool ok = true;
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        const uint32_t buf = i & 1;
-        if (!mbar_wait(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
-        const uint32_t d = tmem_base + buf * kN;
-        for (int g = 0; g < G; ++g, ++it) {
-          const int s = it % S;
-          const int r = sc % SF;
-          const uint32_t sfa = tmem_base + Cfg::kSfCol0 + (sc % TS) * Cfg::kSfSlotCols;
-          if ((g & 3) == 0) {
-            if (!mbar_wait(sfull_bar(r), (sc / SF) & 1u, kSiteScales, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t src = sbase + Cfg::sf + r * Cfg::kSfBytes;
-            tmem_copy_32x128b_x4(sfa, smem_desc_copy32x16(src));
-            tmem_copy_32x128b_x4(sfa + 4, smem_desc_copy32x16(src + Cfg::kSfA));
-            tmem_copy_32x128b_x4(sfa + 8, smem_desc_copy32x16(src + 2 * Cfg::kSfA));
-          }
-          if (!mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) {
+    // The whole warp walks the loop and one lane issues, so that descriptors and addresses live in
+    // uniform registers (from a lane's own registers an MMA takes 64 cycles to issue).
+    const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
+    const uint64_t sf0 = smem_desc_copy32x16(sbase + Cfg::sf);
+    const bool leader = elect_one();
+    uint32_t it = 0, sc = 0;       // groups and scale slots issued so far
+    bool ok = true;
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      const uint32_t buf = i & 1;
+      if (!mbar_wait_warp(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
+      const uint32_t d = tmem_base + buf * kN;
+      for (int g = 0; g < G; ++g, ++it) {
+        const int s = it % S;
+        const int r = sc % SF;
+        const uint32_t sfa = tmem_base + Cfg::kSfCol0 + (sc % TS) * Cfg::kSfSlotCols;
+        if ((g & 3) == 0) {
+          if (!mbar_wait_warp(sfull_bar(r), (sc / SF) & 1u, kSiteScales, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t byte = static_cast<uint32_t>(g & 3);
-          const uint32_t idesc = idesc_e4m3_ue8m0(Cfg::kTileM, kN, byte);
-          const uint32_t sfa_b = sfa | (byte << 30), sfb_b = (sfa + 4) | (byte << 30);
-          const uint32_t a_addr = sbase + Cfg::a + s * Cfg::kABytes;
-          const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
-#pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            mma_f8_ue8m0(d, smem_desc_k_sw128(a_addr + 32 * kk), smem_desc_k_sw128(b_addr + 32 * kk),
-                         idesc, (g > 0 || kk > 0) ? 1u : 0u, sfa_b, sfb_b);
-          mma_commit<1>(empty_bar(s));
-          if ((g & 3) == 3 || g == G - 1) {       // the slot's last group: free it when read
-            mma_commit<1>(sempty_bar(r));
-            ++sc;
+          const uint64_t src = sf0 + r * (Cfg::kSfBytes >> 4);
+          if (leader) {
+            tmem_copy_32x128b_x4(sfa, src);
+            tmem_copy_32x128b_x4(sfa + 4, src + (Cfg::kSfA >> 4));
+            tmem_copy_32x128b_x4(sfa + 8, src + 2 * (Cfg::kSfA >> 4));
           }
         }
-        if (!ok) break;
-        mma_commit<1>(tfull_bar(buf));
+        if (!mbar_wait_warp(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t byte = static_cast<uint32_t>(g & 3);
+        const uint32_t idesc = idesc_e4m3_ue8m0(Cfg::kTileM, kN, byte);
+        const uint32_t sfa_b = sfa | (byte << 30), sfb_b = (sfa + 4) | (byte << 30);
+        const uint64_t a = a0 + s * (Cfg::kABytes >> 4), b = b0 + s * (Cfg::kBBytes >> 4);
+        const bool last_of_slot = (g & 3) == 3 || g == G - 1;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            mma_f8_ue8m0(d, a + 2 * kk, b + 2 * kk, idesc, (g > 0 || kk > 0) ? 1u : 0u, sfa_b, sfb_b);
+          mma_commit<1>(empty_bar(s));
+          if (last_of_slot) mma_commit<1>(sempty_bar(r));   // the slot's last group: free it when read
+        }
+        if (last_of_slot) ++sc;
       }
+      if (!ok) break;
+      if (leader) mma_commit<1>(tfull_bar(buf));
+    }
+    if (leader) {
       mma_commit<1>(drain_bar);
       mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
     }
+    __syncwarp();
   } else if (warp == Cfg::kSfWarp) {
     // -------------------------------------------------------------- scale producer
     // Slots hold four groups of one tile (4k .. 4k + 3; a tile's last slot may be

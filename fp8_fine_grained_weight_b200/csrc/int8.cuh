@@ -241,19 +241,6 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// Wait for a phase by a whole warp; the outcome is warp-uniform (and known to be to the compiler).
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, unsigned int site, volatile int* abort) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, site, abort));
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
 // 1 / (1 + exp(-g)) by the hardware's base-2 exponential and reciprocal: exp within 2 + 0.75 |g|
 // units of 2^-23 (2^-22 for ex2, the rounding of g log2(e) and of the constant), the sum rounded
 // once, the reciprocal within one unit.  For g < -87.3 the divisor passes 2^126 and the result is
