@@ -434,60 +434,58 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, kN);
-        uint32_t it = 0, acc_it = 0;
-        bool ok = true;
-        for (int ui = 0; ok && ui < n_units; ++ui) {
-          const Unit u = unit_at(ui, p, unit0, units, G);
-          uint32_t buf = 0;
-          for (int g = u.g0; g < u.g1; ++g, ++it) {
-            const bool fresh = PROMOTE || g == u.g0;   // a new accumulator for this group
-            const bool publish = PROMOTE || g == u.g1 - 1;
-            const int s = it % S;
-            // The stage's operands first (normally long in place), then the accumulator,
-            // which comes free just in time: nothing should separate its release from
-            // the MMAs.
-            if (!mbar_wait(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) {
+      // The whole warp walks the loop and one lane issues, so that descriptors and addresses
+      // live in uniform registers (from a lane's own an MMA takes 64 cycles to issue).
+      constexpr uint32_t idesc = idesc_e4m3_f32(Cfg::kTileM, kN);
+      const uint64_t a0 = smem_desc_k_sw128(sbase + Cfg::a), b0 = smem_desc_k_sw128(sbase + Cfg::b);
+      const bool leader = elect_one();
+      uint32_t it = 0, acc_it = 0;
+      bool ok = true;
+      for (int ui = 0; ok && ui < n_units; ++ui) {
+        const Unit u = unit_at(ui, p, unit0, units, G);
+        uint32_t buf = 0;
+        for (int g = u.g0; g < u.g1; ++g, ++it) {
+          const bool fresh = PROMOTE || g == u.g0;   // a new accumulator for this group
+          const bool publish = PROMOTE || g == u.g1 - 1;
+          const int s = it % S;
+          // The stage's operands first (normally long in place), then the accumulator,
+          // which comes free just in time: nothing should separate its release from
+          // the MMAs.
+          if (!mbar_wait_warp(full_bar(s), (it / S) & 1u, kSiteMmaFull, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (fresh) {
+            buf = acc_it % NB;
+            if (!mbar_wait_warp(tempty_bar(buf), ((acc_it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) {
               ok = false;
               break;
             }
-            if (fresh) {
-              buf = acc_it % NB;
-              if (!mbar_wait(tempty_bar(buf), ((acc_it / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) {
-                ok = false;
-                break;
-              }
-            }
-            tc_fence_after();
-            const uint32_t d = tmem_base + buf * kN;
-            const uint32_t a_addr = sbase + Cfg::a + s * Cfg::kABytes;
-            const uint32_t b_addr = sbase + Cfg::b + s * Cfg::kBBytes;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * kN;
+          const uint64_t a = a0 + s * (Cfg::kABytes >> 4), b = b0 + s * (Cfg::kBBytes >> 4);
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 32; ++kk) {
               const uint32_t accumulate = PROMOTE ? (kk > 0) : (g > u.g0 || kk > 0);
-              mma_f8<1>(d, smem_desc_k_sw128(a_addr + 32 * kk), smem_desc_k_sw128(b_addr + 32 * kk),
-                        idesc, accumulate);
+              mma_f8<1>(d, a + 2 * kk, b + 2 * kk, idesc, accumulate);
             }
-            if (PROMOTE) {
-              // One commit per group: its arrival on the stage's barrier both frees the
-              // stage for the producer and publishes the group's partial to the epilogue
-              // (group it uses stage it % S and accumulator it % NB).
-              mma_commit<1>(empty_bar(s));
-              ++acc_it;
-            } else {
-              mma_commit<1>(empty_bar(s));
-              if (publish) {
-                mma_commit<1>(tfull_bar(buf));
-                ++acc_it;
-              }
-            }
+            // PROMOTE: one commit per group, whose arrival on the stage's barrier both frees the
+            // stage for the producer and publishes the group's partial to the epilogue
+            // (group it uses stage it % S and accumulator it % NB).
+            mma_commit<1>(empty_bar(s));
+            if (!PROMOTE && publish) mma_commit<1>(tfull_bar(buf));
           }
+          if (publish) ++acc_it;
         }
-        // All MMAs this thread issued complete before TMEM is released.
+      }
+      // All MMAs this warp issued complete before TMEM is released.
+      if (leader) {
         mma_commit<1>(drain_bar);
         mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
       }
+      __syncwarp();
     } else if (warp == 2 && PROMOTE) {
       // ---------------------------------------------------------- scale producer
       // Slot layout: [0, 128) A scales of the tile's 128 rows; then the B scales: the
