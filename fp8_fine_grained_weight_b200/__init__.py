@@ -64,6 +64,8 @@ SIGNATURES = {
     "fp8q_gemm_int8_gated": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp]),
     "fp8_gemm_blockscaled_gated": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
                                           _i64, _i64, _i64, _vp]),
+    "fp8_gemm_gated_ue8m0": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
+                                    _i64, _i64, _i64, _vp]),
     "fp8q_gated_backward_quant": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
                                          _i64, _vp, _i64, _i32, _vp]),
     "fp8q_quant_act_dual_padded": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
@@ -646,6 +648,17 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
     (g, then u) kept for ``gated_backward_quant``.  ``out``: h, or (h, gu) with ``with_gu``, to
     write into.  Any M; N and K multiples of 128; FP32 or power-of-two scales.
     """
+    return _gemm_gated("fp8_gemm_blockscaled_gated", qa, sa, qw, sw, with_gu, out)
+
+
+def gemm_gated_ue8m0(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+                     with_gu: bool = False, out=None):
+    """gemm_blockscaled_gated for power-of-two scales, applied inside the tensor core: the faster of
+    the two.  Scales that are not powers of two are reported through ``device_error``."""
+    return _gemm_gated("fp8_gemm_gated_ue8m0", qa, sa, qw, sw, with_gu, out)
+
+
+def _gemm_gated(entry: str, qa, sa, qw, sw, with_gu: bool, out):
     qa, qw = _u8(qa), _u8(qw)
     M, rows, K, lda, ld_sa, ldw = _gated_operands(qa, sa, qw, sw)
     if rows % 256:
@@ -663,7 +676,7 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
         if with_gu:
             _rows(gu, torch.bfloat16, "gu", M, rows, qa.device)
             ldgu = _pitch(gu)
-    _launch(qa, "fp8_gemm_blockscaled_gated", qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
+    _launch(qa, entry, qa.data_ptr(), sa.data_ptr(), ld_sa, qw.data_ptr(), sw.data_ptr(),
             h.data_ptr(), ldh, gu.data_ptr() if with_gu else None, ldgu, M, N, K, lda, ldw)
     return (h, gu) if with_gu else h
 

@@ -294,6 +294,87 @@ bool encode_bf16_tiles(CUtensorMap* tm, const void* base, int64_t rows, int64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// pow2: the scales are powers of two; others are reported.
+int run_fp8_gated(bool pow2, const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W, const float* sW,
+                  void* H, int64_t ldh, void* GU, int64_t ldgu, int64_t M, int64_t N, int64_t K, int64_t lda,
+                  int64_t ldw, void* stream) {
+  if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
+  if (N > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
+  int st = check_dense_blockscaled(A, sA, ld_sa, W, sW, 0, FP8Q_BSCALE_BLOCK128x128, H, FP8Q_OUT_BF16, M, N, K, lda,
+                                   ldw, ldh);
+  if (st != FP8Q_OK) return st;
+  if (GU != nullptr) {
+    if (ldgu < 2 * N) return FP8Q_ERR_SHAPE;
+    if (ldgu % 8 != 0 || !aligned(GU, 16)) return FP8Q_ERR_ALIGN;
+  }
+  const auto s = static_cast<cudaStream_t>(stream);
+  const int sms = sm_count();
+  if (sms <= 0) return FP8Q_ERR_CUDA;
+  if (few_rows(M, 2 * N, K / 128, sms, true)) {
+    constexpr int KIND = fp8q::kSkinnyFp8;
+    const int mp = skinny_rows(M, 64);
+    SkinnyArgs a{};
+    a.sA = sA; a.ld_sa = ld_sa; a.sB = sW; a.C = H; a.ldc = ldh;
+    a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+    a.vec = 1;
+    a.pow2 = pow2;
+    const int64_t units = plan_skinny<true>(&a, mp, sms);
+    if (units == 0) return FP8Q_ERR_SHAPE;
+    CUtensorMap tmA, tmW;
+    if ((st = encode_operand(&tmA, A, K, M, lda, mp)) != FP8Q_OK ||
+        (st = encode_operand(&tmW, W, K, 2 * N, ldw, 64)) != FP8Q_OK)
+      return st;
+    switch (mp) {
+      case 16: return launch_skinny<KIND, true, true, 16>(tmA, tmW, a, units, s);
+      case 32: return launch_skinny<KIND, true, true, 32>(tmA, tmW, a, units, s);
+      default: return launch_skinny<KIND, true, true, 64>(tmA, tmW, a, units, s);
+    }
+  }
+  if (pow2) {
+    using Cfg = fp8q::Ue8m0Cfg<false, true>;
+    static constexpr auto kern = fp8q::gemm_fp8_ue8m0_kernel<false, true, false, true>;
+    const int64_t tiles = ((M + Cfg::kTileM - 1) / Cfg::kTileM) * ((N + Cfg::kOutN - 1) / Cfg::kOutN);
+    if (tiles > kMaxTiles) return FP8Q_ERR_SHAPE;
+    CUtensorMap tmA, tmW;
+    if ((st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM)) != FP8Q_OK ||
+        (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kOutN)) != FP8Q_OK)
+      return st;
+    GemmArgs a{};
+    a.sA = sA; a.ld_sa = ld_sa; a.sB = sW; a.C = H; a.ldc = ldh;
+    a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu;
+    a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+    a.n_fastest = M > 2 * N;
+    const int units = resident_ctas<kern>(Cfg::kThreads, Cfg::smem_bytes);
+    if (units <= 0) return FP8Q_ERR_CUDA;
+    kern<<<static_cast<unsigned>(tiles < units ? tiles : units), Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
+    return launched();
+  }
+  using Cfg = fp8q::GatedCfg;
+  GatedArgs a{};
+  a.sA = sA; a.ld_sa = ld_sa; a.sW = sW;
+  a.h = static_cast<__nv_bfloat16*>(H); a.ldh = ldh;
+  a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
+  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + Cfg::kTileN - 1) / Cfg::kTileN;
+  if (mt * nt > kMaxTiles) return FP8Q_ERR_SHAPE;
+  a.mt = static_cast<int>(mt);
+  a.nt = static_cast<int>(nt);
+  a.n_fastest = M > 2 * N;
+  CUtensorMap tmA, tmW;
+  if ((st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM)) != FP8Q_OK ||
+      (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kTileN)) != FP8Q_OK)
+    return st;
+  static constexpr auto plain = fp8q::gemm_fp8_gated_kernel<false>, keep = fp8q::gemm_fp8_gated_kernel<true>;
+  const int units = GU != nullptr ? resident_ctas<keep>(Cfg::kThreads, Cfg::smem_bytes)
+                                  : resident_ctas<plain>(Cfg::kThreads, Cfg::smem_bytes);
+  if (units <= 0) return FP8Q_ERR_CUDA;
+  const auto grid = static_cast<unsigned>(mt * nt < units ? mt * nt : units);
+  if (GU != nullptr)
+    keep<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
+  else
+    plain<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
+  return launched();
+}
+
 }  // namespace
 
 extern "C" {
@@ -341,62 +422,13 @@ int fp8q_gemm_int8_gated(const int8_t* A, const float* sA, const int8_t* W, cons
 int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W, const float* sW,
                                void* H, int64_t ldh, void* GU, int64_t ldgu, int64_t M, int64_t N, int64_t K,
                                int64_t lda, int64_t ldw, void* stream) {
-  using Cfg = fp8q::GatedCfg;
-  if (M == 0 && N >= 0 && K >= 0) return FP8Q_OK;
-  if (N > 0x3FFFFFFF) return FP8Q_ERR_SHAPE;
-  int st = check_dense_blockscaled(A, sA, ld_sa, W, sW, 0, FP8Q_BSCALE_BLOCK128x128, H, FP8Q_OUT_BF16, M, N, K, lda,
-                                   ldw, ldh);
-  if (st != FP8Q_OK) return st;
-  if (GU != nullptr) {
-    if (ldgu < 2 * N) return FP8Q_ERR_SHAPE;
-    if (ldgu % 8 != 0 || !aligned(GU, 16)) return FP8Q_ERR_ALIGN;
-  }
-  const int sms = sm_count();
-  if (sms <= 0) return FP8Q_ERR_CUDA;
-  if (few_rows(M, 2 * N, K / 128, sms, true)) {
-    constexpr int KIND = fp8q::kSkinnyFp8;
-    const int mp = skinny_rows(M, 64);
-    SkinnyArgs a{};
-    a.sA = sA; a.ld_sa = ld_sa; a.sB = sW; a.C = H; a.ldc = ldh;
-    a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
-    a.vec = 1;
-    const int64_t units = plan_skinny<true>(&a, mp, sms);
-    if (units == 0) return FP8Q_ERR_SHAPE;
-    CUtensorMap tmA, tmW;
-    if ((st = encode_operand(&tmA, A, K, M, lda, mp)) != FP8Q_OK ||
-        (st = encode_operand(&tmW, W, K, 2 * N, ldw, 64)) != FP8Q_OK)
-      return st;
-    const auto s = static_cast<cudaStream_t>(stream);
-    switch (mp) {
-      case 16: return launch_skinny<KIND, true, true, 16>(tmA, tmW, a, units, s);
-      case 32: return launch_skinny<KIND, true, true, 32>(tmA, tmW, a, units, s);
-      default: return launch_skinny<KIND, true, true, 64>(tmA, tmW, a, units, s);
-    }
-  }
-  GatedArgs a{};
-  a.sA = sA; a.ld_sa = ld_sa; a.sW = sW;
-  a.h = static_cast<__nv_bfloat16*>(H); a.ldh = ldh;
-  a.gu = static_cast<__nv_bfloat16*>(GU); a.ld_gu = ldgu; a.M = M; a.N = N; a.G = static_cast<int>(K / 128);
-  const int64_t mt = (M + Cfg::kTileM - 1) / Cfg::kTileM, nt = (N + Cfg::kTileN - 1) / Cfg::kTileN;
-  if (mt * nt > kMaxTiles) return FP8Q_ERR_SHAPE;
-  a.mt = static_cast<int>(mt);
-  a.nt = static_cast<int>(nt);
-  a.n_fastest = M > 2 * N;
-  CUtensorMap tmA, tmW;
-  if ((st = encode_operand(&tmA, A, K, M, lda, Cfg::kTileM)) != FP8Q_OK ||
-      (st = encode_operand(&tmW, W, K, 2 * N, ldw, Cfg::kTileN)) != FP8Q_OK)
-    return st;
-  const auto s = static_cast<cudaStream_t>(stream);
-  static constexpr auto plain = fp8q::gemm_fp8_gated_kernel<false>, keep = fp8q::gemm_fp8_gated_kernel<true>;
-  const int units = GU != nullptr ? resident_ctas<keep>(Cfg::kThreads, Cfg::smem_bytes)
-                                  : resident_ctas<plain>(Cfg::kThreads, Cfg::smem_bytes);
-  if (units <= 0) return FP8Q_ERR_CUDA;
-  const auto grid = static_cast<unsigned>(mt * nt < units ? mt * nt : units);
-  if (GU != nullptr)
-    keep<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
-  else
-    plain<<<grid, Cfg::kThreads, Cfg::smem_bytes, s>>>(tmA, tmW, a);
-  return launched();
+  return run_fp8_gated(false, A, sA, ld_sa, W, sW, H, ldh, GU, ldgu, M, N, K, lda, ldw, stream);
+}
+
+int fp8_gemm_gated_ue8m0(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W, const float* sW, void* H,
+                         int64_t ldh, void* GU, int64_t ldgu, int64_t M, int64_t N, int64_t K, int64_t lda,
+                         int64_t ldw, void* stream) {
+  return run_fp8_gated(true, A, sA, ld_sa, W, sW, H, ldh, GU, ldgu, M, N, K, lda, ldw, stream);
 }
 
 int fp8q_gated_backward_quant(const void* dH, int64_t lddh, const void* GU, int64_t ldgu, int64_t M, int64_t N,
@@ -487,8 +519,8 @@ int fp8q_gated_linear_forward(const void* x, const void* w, int64_t T, int64_t N
     st = (l.Tp == T ? fp8q_quant_act_dual : fp8q_quant_act_dual_padded)(
         x, T, K, K, s8 + l.qx, K, f32(s8 + l.sx), T, k8 + l.qxt, l.Tp, f32(k8 + l.sxt), K, pow2_scale, stream);
   if (st != FP8Q_OK) return st;
-  return fp8_gemm_blockscaled_gated(s8 + l.qx, f32(s8 + l.sx), T, k8 + l.qw, f32(k8 + l.sw), H, N, k8 + l.gu, R, T, N,
-                                    K, K, K, stream);
+  return (pow2_scale ? fp8_gemm_gated_ue8m0 : fp8_gemm_blockscaled_gated)(
+      s8 + l.qx, f32(s8 + l.sx), T, k8 + l.qw, f32(k8 + l.sw), H, N, k8 + l.gu, R, T, N, K, K, K, stream);
 }
 
 int fp8q_gated_linear_backward(const void* dH, const void* kept, int64_t T, int64_t N, int64_t K, int for_dw,

@@ -235,8 +235,9 @@ __global__ void __launch_bounds__(GatedCfg::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsEpi));
     // ------------------------------------------------------------ promotion + epilogue
-    // With two warps on a scheduler every dependent instruction of this loop costs its whole latency, so it is kept short: running indices instead of divisions, one vector
-    // load for four groups' scales, one arrival per warp, one vote per wait.
+    // With two warps on a scheduler every dependent instruction of this loop costs its whole
+    // latency, so it is kept short: running indices instead of divisions, one vector load for four
+    // groups' scales, one arrival per warp, one vote per wait.
     const int quad = warp & 3, set = (warp - kEpiWarp0) >> 2;
     const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + set * Cfg::kSetCols;
     uint32_t s = 0, phase = 0, buf = 0, r = 0, rphase = 0;

@@ -106,6 +106,9 @@ struct GemmArgs {
   float* sc;
   int64_t ld_sc;
   int qpow2;
+  // Gated product (power-of-two scales): g and u in bf16, [M, 2N], when set.
+  __nv_bfloat16* gu;
+  int64_t ld_gu;
   // Dense tile order: m fastest (0), so that the CTAs of a wave share B tiles and re-read
   // A once per wave, or n fastest (1), the reverse; the host takes n fastest when A is
   // the larger operand (M > N).

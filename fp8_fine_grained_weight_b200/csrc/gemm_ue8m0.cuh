@@ -17,6 +17,15 @@
 // (kSiteScaleFormat << 8) | FP8Q_ERR_SCALE in the device error word for them and goes on
 // with scale 1.
 //
+// GATED: the gated feed-forward projections, h = silu(g) u with g and u the products with the
+// gate's N rows of B and the N rows after them (B is [2N, K]); p.gu takes g and u in bf16 when
+// set.  Tiles of 128 columns of h, 128 gate and 128 up columns in one accumulator of 256 columns:
+// there is room for one only, and the epilogue frees it as soon as it is in registers, before the
+// activation and the stores.  Measured at 8192 x 2048 x 7168: 178 us, 201 us with g and u kept
+// (promoted, gated.cuh: 225 and 253), 29 us at 1000 rows (38).  Two accumulators of 192 columns
+// measured 212 and 46 us: the loads bound it, 64 bytes a clock into an SM, and a tile of 256 columns
+// reads 48 KB per K-group for 4.2 MMACs where one of 192 reads 40 KB for 3.1.
+//
 // Tiles of 128 x 224 (224 divides 7168; two 224-column FP32 accumulators and the scale
 // region fill the 512 TMEM columns), persistent CTAs, 12 warps.  GROUPED: the MoE form of
 // fp8_gemm_grouped -- tiles come from a per-expert table built from m_offsets on the
@@ -49,18 +58,21 @@
 #include <cuda_bf16.h>
 #include "ptx.cuh"
 #include "gemm.cuh"
+#include "silu.cuh"
 
 namespace fp8q {
 
 constexpr unsigned int kSiteScaleFormat = 8;
 constexpr unsigned int kErrScale = 7;            // FP8Q_ERR_SCALE
 
-template <bool GROUPED>
+template <bool GROUPED, bool GATED = false>
 struct Ue8m0Cfg {
   static constexpr int kTileM = 128;
-  static constexpr int kN = 224;                  // tile columns = MMA N
-  static constexpr int kStages = GROUPED ? 4 : 5; // grouped: room for the tile table
-  static constexpr int kAccCols = 2 * kN;         // two accumulator buffers
+  static constexpr int kN = GATED ? 256 : 224;    // tile columns = MMA N; GATED: 128 gate, 128 up
+  static constexpr int kOutN = GATED ? kN / 2 : kN;      // output columns per tile
+  static constexpr int kStages = GROUPED || GATED ? 4 : 5;   // grouped: room for the tile table
+  static constexpr int kAccBufs = GATED ? 1 : 2;
+  static constexpr int kAccCols = kAccBufs * kN;
   static constexpr int kSfSmemSlots = 3;          // scale slots in shared memory, 4 groups each
   static constexpr int kSfTmemSlots = 4;          // scale slots in TMEM
   static constexpr int kSfSlotCols = 12;          // A: 4 columns, B: 8
@@ -87,6 +99,7 @@ struct Ue8m0Cfg {
   static_assert((kN + 31) / 32 <= 8, "B scales fit two copy blocks");
   static_assert(kN % 16 == 0 && kN <= 256, "MMA N for M = 128");
   static_assert(kSetCols % 16 == 0, "16-column epilogue loads");
+  static_assert(!GATED || kOutN == 128, "one weight scale for either projection of a tile");
   static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0 && sf % 1024 == 0, "alignment");
   static_assert(smem_bytes <= 232448, "fits the 227 KB opt-in shared memory");
 };
@@ -120,15 +133,17 @@ __device__ __forceinline__ uint32_t ue8m0_of(float s, bool& bad) {
   return 127;
 }
 
-template <bool ROW_B, bool OUT_BF16, bool GROUPED>
-__global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
+template <bool ROW_B, bool OUT_BF16, bool GROUPED, bool GATED = false>
+__global__ void __launch_bounds__(Ue8m0Cfg<GROUPED, GATED>::kThreads, 1)
     gemm_fp8_ue8m0_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB, const GemmArgs p) {
-  using Cfg = Ue8m0Cfg<GROUPED>;
+  using Cfg = Ue8m0Cfg<GROUPED, GATED>;
+  static_assert(!GATED || (OUT_BF16 && !ROW_B && !GROUPED), "the gated product is dense, bf16, with block scales");
   static_assert(!(GROUPED && ROW_B), "grouped GEMMs take 128x128 weight-block scales");
   constexpr int S = Cfg::kStages;
   constexpr int SF = Cfg::kSfSmemSlots;
   constexpr int TS = Cfg::kSfTmemSlots;
+  constexpr uint32_t NB = Cfg::kAccBufs;
   constexpr int kN = Cfg::kN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < NB; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), 32 * Cfg::kEpiWarps);   // every epilogue thread
     }
@@ -173,7 +188,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
     tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish<1>();
   }
-  const int nt_total = static_cast<int>((p.N + kN - 1) / kN);
+  const int nt_total = static_cast<int>((p.N + Cfg::kOutN - 1) / Cfg::kOutN);
   int* sched = reinterpret_cast<int*>(smem + Cfg::sched);
   int mt_total = 0, num_tiles = 0;
   if (!GROUPED) {
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
   // of a wave share B tiles; grouped: expert by expert, n-fastest inside an expert.
   const int n_tiles = blockIdx.x < num_tiles ? (num_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
   auto tile_of = [&](int i) -> Tile {
-    return decode_tile<GROUPED, Cfg::kTileM, kN>(blockIdx.x + i * gridDim.x, p, mt_total, nt_total, sched);
+    return decode_tile<GROUPED, Cfg::kTileM, Cfg::kOutN>(blockIdx.x + i * gridDim.x, p, mt_total, nt_total, sched);
   };
 
   if (warp == 0) {
@@ -223,6 +238,9 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
                       static_cast<int32_t>(tl.row0));
           tma_load_2d(sbase + Cfg::b + s * Cfg::kBBytes, &tmB, full_bar(s), g * kBK,
                       static_cast<int32_t>(tl.brow0));
+          if (GATED)                                     // the box is kOutN rows: the up projection's too
+            tma_load_2d(sbase + Cfg::b + s * Cfg::kBBytes + Cfg::kOutN * kBK, &tmB, full_bar(s), g * kBK,
+                        static_cast<int32_t>(p.N + tl.brow0));
         }
       }
       // every issued load lands before the CTA can exit (bounded; loads end on their own)
@@ -239,8 +257,8 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
     uint32_t it = 0, sc = 0;       // groups and scale slots issued so far
     bool ok = true;
     for (int i = 0; ok && i < n_tiles; ++i) {
-      const uint32_t buf = i & 1;
-      if (!mbar_wait_warp(tempty_bar(buf), ((i >> 1) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
+      const uint32_t buf = i % NB;
+      if (!mbar_wait_warp(tempty_bar(buf), ((i / NB) & 1u) ^ 1u, kSiteMmaEmpty, abort_flag)) break;
       const uint32_t d = tmem_base + buf * kN;
       for (int g = 0; g < G; ++g, ++it) {
         const int s = it % S;
@@ -295,6 +313,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
     //   B, 128x128 blocks: the tile's 224 rows touch at most 3 blocks; lane l < 12 loads
     //     block nb0 + l / 4, group 4k + l % 4, and shuffles build the packed words (every
     //     32-row chunk of the tile lies inside one block).
+    //   GATED: the gate's block in lanes 0-3, the up projection's in lanes 4-7.
     //   B, 1x128 rows: lane l loads the 4 groups' scales of rows l + 32j, j < 7.
     constexpr int kRawB = ROW_B ? 28 : 1;
     struct Raw {
@@ -328,6 +347,10 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
             if (g < G && n < p.N) raw.b[4 * j + b] = __ldg(p.sB + static_cast<int64_t>(g) * p.ld_sb + n);
           }
         }
+      } else if (GATED) {
+        // lane b < 4: the gate's scale in group 4k + b; lane 4 + b: the up projection's
+        const int g = 4 * k + (lane & 3);
+        if (lane < 8 && g < G) raw.b[0] = __ldg(p.sB + (tl.col0 + (lane >> 2) * p.N) / 128 * G + g);
       } else {
         const int64_t nb = tl.col0 / 128 + (lane >> 2);
         const int g = 4 * k + (lane & 3);
@@ -353,6 +376,13 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
 #pragma unroll
           for (int b = 0; b < 4; ++b) wb[j] |= ue8m0_of(raw.b[4 * j + b], bad) << (8 * b);
         }
+      } else if (GATED) {
+        const uint32_t byte = ue8m0_of(raw.b[0], bad);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int b = 0; b < 8; ++b) w[b >> 2] |= __shfl_sync(0xFFFFFFFFu, byte, b) << (8 * (b & 3));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wb[j] = w[j >> 2];
       } else {
         const uint32_t byte = ue8m0_of(raw.b[0], bad);
         uint32_t w[3];
@@ -369,7 +399,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
           wb[j] = jb == 0 ? w[0] : (jb == 1 ? w[1] : w[2]);
         }
       }
-      wb[7] = 0;
+      if (!GATED) wb[7] = 0;
       const int r = static_cast<int>(sc % SF);
       // warp-uniform outcome (the warp writes the slot together)
       const bool got = mbar_wait(sempty_bar(r), static_cast<uint32_t>(((sc / SF) & 1) ^ 1), kSiteScales,
@@ -405,12 +435,48 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED>::kThreads, 1)
     bool ok = true;
     for (int i = 0; i < n_tiles; ++i) {
       const Tile tl = tile_of(i);
-      const uint32_t buf = i & 1;
+      const uint32_t buf = i % NB;
       // warp-uniform outcome: the TMEM loads below are whole-warp instructions
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar(buf), (i >> 1) & 1u, kSiteEpilogue, abort_flag));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar(buf), (i / NB) & 1u, kSiteEpilogue, abort_flag));
       if (!ok) break;
       tc_fence_after();
       const int64_t m = tl.row0 + 32 * q + lane;
+      if constexpr (GATED) {
+        // 64 columns of h per warpgroup, whose accumulator is free once it is in registers
+        const bool row_ok = m < tl.row_end;
+        const uint32_t t0 = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + 64 * set;
+        const int64_t n0 = tl.col0 + 64 * set;
+        uint32_t rg[64], ru[64];
+        tmem_ld_64cols(t0, rg);
+        tmem_ld_64cols(t0 + Cfg::kOutN, ru);
+        tmem_ld_wait_regs(rg);
+        tmem_ld_wait_regs(ru);
+        tc_fence_before();
+        mbar_arrive(tempty_bar(buf));
+        uint4 v[8];
+        auto pack = [&](auto value) {                      // columns 2i, 2i + 1 as bf16
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              __nv_bfloat162 h = __floats2bfloat162_rn(value(8 * j + 2 * t), value(8 * j + 2 * t + 1));
+              w[t] = *reinterpret_cast<uint32_t*>(&h);
+            }
+            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        };
+        if (p.gu != nullptr) {
+          uint8_t* grow = reinterpret_cast<uint8_t*>(p.gu + m * p.ld_gu + n0);
+          pack([&](int i) { return __uint_as_float(rg[i]); });
+          store_rows_by_quads(v, grow, row_ok);
+          pack([&](int i) { return __uint_as_float(ru[i]); });
+          store_rows_by_quads(v, grow + 2 * p.N, row_ok);
+        }
+        pack([&](int i) { return silu_mul(__uint_as_float(rg[i]), __uint_as_float(ru[i])); });
+        store_rows_by_quads(v, reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(p.C) + m * p.ldc + n0), row_ok);
+        continue;
+      }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kN +
                              set * Cfg::kSetCols;
       const int64_t n_set = tl.col0 + set * Cfg::kSetCols;

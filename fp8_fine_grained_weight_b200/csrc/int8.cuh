@@ -7,6 +7,7 @@
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "gemm.cuh"
+#include "silu.cuh"
 
 namespace fp8q {
 
@@ -240,19 +241,6 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-
-// 1 / (1 + exp(-g)) by the hardware's base-2 exponential and reciprocal: exp within 2 + 0.75 |g|
-// units of 2^-23 (2^-22 for ex2, the rounding of g log2(e) and of the constant), the sum rounded
-// once, the reciprocal within one unit.  For g < -87.3 the divisor passes 2^126 and the result is
-// returned as 0; silu(g) is above -1.2e-36 there.
-__device__ __forceinline__ float sigmoid(float g) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return r;
-}
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid(g) * u; }
 
 // 32 x 32 words, row i in lane i's v[0 .. 31], transposed in place: afterwards lane i holds
 // column i.  Five exchange stages; registers are indexed by constants only.

@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 #include "ptx.cuh"
 #include "gemm.cuh"
+#include "gemm_ue8m0.cuh"
 #include "int8.cuh"
 
 namespace fp8q {
@@ -55,6 +56,7 @@ struct SkinnyArgs {
   int nt;               // weight tiles
   int split;            // CTAs per cluster, at most kMaxSplit
   int vec;              // C takes four elements at a time
+  int pow2;             // FP8: report scales that are not powers of two
 };
 
 constexpr int kMaxSplit = 4;
@@ -239,6 +241,16 @@ __global__ void __launch_bounds__(256, 2)
       cp_async_arrive(sfull_bar(r));
     }
     cp_async_wait_all();
+  } else if (FP8 && warp == 3) {
+    if (p.pow2) {
+      bool bad = false;
+      const float* sW = p.sB + (col0 + (lane & 1) * p.N) / 128 * p.G + g0;
+      for (int i = lane >> 1; i < n_g; i += 16) ue8m0_of(__ldg(sW + i), bad);
+      for (int it = 0; it < n_g; ++it)
+        for (int64_t m = row0 + lane; m < row0 + MP && m < p.M; m += 32)
+          ue8m0_of(__ldg(p.sA + static_cast<int64_t>(g0 + it) * p.ld_sa + m), bad);
+      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) record_error((kSiteScaleFormat << 8) | kErrScale);
+    }
   } else if (!FP8 && warp == 2) {
     // read after the cluster barrier below
     for (int m = lane; m < MP; m += 32) sring[m] = row0 + m < p.M ? __ldg(p.sA + row0 + m) : 0.0f;

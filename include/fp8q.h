@@ -361,6 +361,15 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
                                void* stream);
 
 /*
+ * fp8_gemm_blockscaled_gated for power-of-two scales [P2], applied inside the tensor core as by
+ * fp8_gemm_blockscaled_ue8m0 (with few rows as by fp8_gemm_blockscaled_gated).  Scales that are
+ * not powers of two are reported in the device error word, as there.
+ */
+int fp8_gemm_gated_ue8m0(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W,
+                         const float* sW, void* H, int64_t ldh, void* GU, int64_t ldgu, int64_t M,
+                         int64_t N, int64_t K, int64_t lda, int64_t ldw, void* stream);
+
+/*
  * Backward pass of the gated product, fused with the quantization of its result [Q], [P2].
  * From dH [M, N] and GU [M, 2N] (g, then u), all bf16, with sg = 1 / (1 + exp(-g)):
  *   dg = dH u sg (1 + g (1 - sg)),  du = dH g sg      in FP32, rounded to bf16,
@@ -397,7 +406,8 @@ int fp8q_quant_act_dual_padded(const void* x_bf16, int64_t M, int64_t K, int64_t
  * same in all three calls.
  *
  * forward   quantizes X (1x128; with for_dw also X^T) and W (128x128), H by
- *           fp8_gemm_blockscaled_gated; keeps g, u, the codes of W and of X^T
+ *           fp8_gemm_blockscaled_gated (power-of-two scales: fp8_gemm_gated_ue8m0);
+ *           keeps g, u, the codes of W and of X^T
  * backward  fp8q_gated_backward_quant, then dX = D W (K = 2N) unless dX is NULL, and
  *           dW = D^T X (K = T rounded up to 128) unless dW is NULL, by the block-scaled GEMMs
  *           (power-of-two scales: fp8_gemm_blockscaled_ue8m0)

@@ -64,8 +64,9 @@ def test_gemm_int8_gated_refusals(L):
     assert call(ldw=100) == call(H=P_MIS) == ALIGN
 
 
-def test_gemm_blockscaled_gated_refusals(L):
-    call = caller(L.fp8_gemm_blockscaled_gated, A=P16, sA=P16, ld_sa=4, W=P16, sW=P16, H=P16, ldh=256, GU=P16,
+@pytest.mark.parametrize("entry", ["fp8_gemm_blockscaled_gated", "fp8_gemm_gated_ue8m0"])
+def test_gemm_blockscaled_gated_refusals(L, entry):
+    call = caller(getattr(L, entry), A=P16, sA=P16, ld_sa=4, W=P16, sW=P16, H=P16, ldh=256, GU=P16,
                   ldgu=512, M=4, N=256, K=128, lda=128, ldw=128, stream=NULL)
     assert call(M=0) == OK
     assert call(N=200) == call(K=100) == call(M=-1) == call(N=1 << 30, ldh=1 << 30) == SHAPE

@@ -127,6 +127,66 @@ def test_forward_strides_and_guards(fq, M):
     assert (H == 7).all() and (GU == 7).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 128, 128), (65, 128, 640), (100, 256, 512), (127, 384, 128), (129, 640, 1152),
+                                   (300, 256, 1280), (513, 128, 384), (1025, 896, 256), (2500, 1280, 256),
+                                   (130, 10240, 128)])
+def test_forward_of_powers_of_two(fq, M, N, K):
+    """Scales inside the tensor core: part groups of a scale slot, column tiles that end inside a
+    tile of 96 and weight blocks that begin inside one, more tiles than SMs, both tile orders."""
+    import torch
+    _, _, (qa, sa), (qw, sw) = operands(M, N, K, True, M + N + K)
+    C, T = oracle.gemm_blockscaled_ref(qa, sa, qw, sw)
+    args = [to_dev(t) for t in (qa, sa, qw, sw)]
+    h, gu = fq.gemm_gated_ue8m0(*args, with_gu=True)
+    h2 = fq.gemm_gated_ue8m0(*args)
+    torch.cuda.synchronize()
+    assert fq.device_error() == 0
+    check_h(host(h), C, T)
+    assert torch.equal(h, h2)
+    assert_gemm_close("gu", host(gu), C, T, bf16=True)
+
+
+@pytest.mark.parametrize("M", [3, 70, 140])
+def test_forward_of_powers_of_two_strides_and_guards(fq, M):
+    import torch
+    N, K = 256, 384
+    _, _, (qa, sa), (qw, sw) = operands(M, N, K, True, M)
+    C, T = oracle.gemm_blockscaled_ref(qa, sa, qw, sw)
+    A = torch.full((M, K + 32), 0x7F, dtype=torch.uint8, device="cuda")
+    A[:, :K] = to_dev(qa)
+    W = torch.full((2 * N, K + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    W[:, :K] = to_dev(qw)
+    S = torch.full((K // 128, M + 7), float("nan"), device="cuda")
+    S[:, :M] = to_dev(sa)
+    H = torch.full((M + 2, N + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    GU = torch.full((M + 2, 2 * N + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    h, gu = H[1:M + 1, 8:8 + N], GU[1:M + 1, 8:8 + 2 * N]
+    fq.gemm_gated_ue8m0(A[:, :K], S, W[:, :K], to_dev(sw), with_gu=True, out=(h, gu))
+    assert fq.device_error() == 0
+    check_h(host(h), C, T)
+    assert_gemm_close("gu", host(gu.contiguous()), C, T, bf16=True)
+    h2 = torch.empty_like(h)
+    fq.gemm_gated_ue8m0(A[:, :K], S, W[:, :K], to_dev(sw), out=h2)
+    assert torch.equal(h, h2)
+    h.fill_(7.0)
+    gu.fill_(7.0)
+    assert (H == 7).all() and (GU == 7).all()
+
+
+def test_forward_of_powers_of_two_reports_other_scales(fq):
+    """A scale that is no power of two, of a token, of the gate's rows or of the up projection's."""
+    import torch
+    _, _, (qa, sa), (qw, sw) = operands(200, 128, 256, True, 4)
+    for which, at in ((0, (1, 150)), (1, (0, 1)), (1, (1, 0))):
+        scales = [sa.copy(), sw.copy()]
+        scales[which][at] *= 1.5
+        a = [to_dev(t) for t in (qa, scales[0], qw, scales[1])]
+        fq.gemm_gated_ue8m0(*a)
+        assert fq.device_error() == (8 << 8) | 7
+        fq.gemm_gated_ue8m0(*[to_dev(t) for t in (qa, sa, qw, sw)])
+        assert fq.device_error() == 0
+
+
 # -------------------------------------------------------------------------------- backward
 
 def grads64(dh, gu):
@@ -294,7 +354,8 @@ def layer_check(fq, T, N, K, pow2, seed):
     assert h.dtype == dx.dtype == dw.dtype == torch.bfloat16 and dx.shape == x.shape and dw.shape == w.shape
     C, Tm = oracle.gemm_blockscaled_ref(qx, sx, qw, sw)
     check_h(host(h), C, Tm)
-    _, gu = fq.gemm_blockscaled_gated(*[to_dev(t) for t in (qx, sx, qw, sw)], with_gu=True)
+    gated = fq.gemm_gated_ue8m0 if pow2 else fq.gemm_blockscaled_gated          # as the layer
+    _, gu = gated(*[to_dev(t) for t in (qx, sx, qw, sw)], with_gu=True)
     q, s, qt, st = (host(t) for t in fq.gated_backward_quant(dh, gu, pow2))
     qwt, swt = oracle.quant_weight_128x128(np.ascontiguousarray(wb.T), pow2)
     C, Tm = oracle.gemm_blockscaled_ref(q, s, qwt, swt)
