@@ -41,14 +41,14 @@
 //                tcgen05.mma of one thread run in issue order, so a scale slot in TMEM is
 //                rewritten only after the MMAs that read it.  Commits free smem stages,
 //                scale slots and finished accumulators.
-//   warp 2       scale producer.  For a slot (groups 4k .. 4k+3 of one tile) lane l packs
-//                the UE8M0 bytes of A rows l, 32+l, 64+l, 96+l (byte j = group 4k+j) into
-//                one 16-byte row of the A block, and those of B rows l + 32j (j < 7) into
-//                two 16-byte rows of the B blocks, in a 3-slot shared-memory ring.  After
+//   warps 2, 3   scale producers of A and of B.  For a slot (groups 4k .. 4k+3 of one tile) lane
+//                l of warp 2 packs the UE8M0 bytes of A rows l, 32+l, 64+l, 96+l (byte j =
+//                group 4k+j) into one 16-byte row of the A block, and warp 3 those of B rows
+//                l + 32j (j < 7) into two 16-byte rows of the B blocks, in a 3-slot
+//                shared-memory ring.  After
 //                the copies the MMA reads, for A row m, lane m and column m/32, and for B
 //                row n, column 4 + n/32 and lane n % 32 of its own sub-partition: the
 //                layout of kind::mxf8f6f4 scale factors (checked on B200 with probes).
-//   warp 3       idle.
 //   warps 4-11   epilogue: warp w drains TMEM lanes 32*(w%4).. and 112 of the 224
 //                columns of a finished accumulator, converts and stores C, and frees the
 //                buffer for the tile after next.
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED, GATED>::kThreads, 1)
       mbar_init(tempty_bar(b), 32 * Cfg::kEpiWarps);   // every epilogue thread
     }
     for (int r = 0; r < SF; ++r) {
-      mbar_init(sfull_bar(r), 1);                       // the scale producer
+      mbar_init(sfull_bar(r), 2);                       // the scale producers
       mbar_init(sempty_bar(r), 1);                      // the MMA thread's commit
     }
     mbar_init(drain_bar, 1);
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED, GATED>::kThreads, 1)
       mbar_wait(drain_bar, 0, kSiteDrain, nullptr);
     }
     __syncwarp();
-  } else if (warp == Cfg::kSfWarp) {
-    // -------------------------------------------------------------- scale producer
+  } else if (warp < Cfg::kEpiWarp0) {
+    // -------------------------------------------------------------- scale producers, A and B
     // Slots hold four groups of one tile (4k .. 4k + 3; a tile's last slot may be
     // partial); the CTA's slots run in order (tile i, slot k), and the raw scales of the
     // next slot are loaded before the current one is stored.
@@ -315,76 +315,76 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED, GATED>::kThreads, 1)
     //     32-row chunk of the tile lies inside one block).
     //   GATED: the gate's block in lanes 0-3, the up projection's in lanes 4-7.
     //   B, 1x128 rows: lane l loads the 4 groups' scales of rows l + 32j, j < 7.
-    constexpr int kRawB = ROW_B ? 28 : 1;
+    const bool of_a = warp == Cfg::kSfWarp;
+    constexpr int kRaw = ROW_B ? 28 : 16;
     struct Raw {
-      float a[16];
-      float b[kRawB];
+      float v[kRaw];
     };
     bool bad = false;
     auto fetch = [&](int i, int k, Raw& raw) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) raw.a[j] = 1.0f;
-#pragma unroll
-      for (int j = 0; j < kRawB; ++j) raw.b[j] = 1.0f;
+      for (int j = 0; j < kRaw; ++j) raw.v[j] = 1.0f;
       if (i >= n_tiles) return;
       const Tile tl = tile_of(i);
+      if (of_a) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = tl.row0 + 32 * j + lane;
+        for (int j = 0; j < 4; ++j) {
+          const int64_t m = tl.row0 + 32 * j + lane;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int g = 4 * k + b;
-          if (g < G && m < tl.row_end) raw.a[4 * j + b] = __ldg(p.sA + static_cast<int64_t>(g) * p.ld_sa + m);
+          for (int b = 0; b < 4; ++b) {
+            const int g = 4 * k + b;
+            if (g < G && m < tl.row_end) raw.v[4 * j + b] = __ldg(p.sA + static_cast<int64_t>(g) * p.ld_sa + m);
+          }
         }
-      }
-      if (ROW_B) {
+      } else if (ROW_B) {
 #pragma unroll
         for (int j = 0; j < 7; ++j) {
           const int64_t n = tl.col0 + 32 * j + lane;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int g = 4 * k + b;
-            if (g < G && n < p.N) raw.b[4 * j + b] = __ldg(p.sB + static_cast<int64_t>(g) * p.ld_sb + n);
+            if (g < G && n < p.N) raw.v[4 * j + b] = __ldg(p.sB + static_cast<int64_t>(g) * p.ld_sb + n);
           }
         }
       } else if (GATED) {
         // lane b < 4: the gate's scale in group 4k + b; lane 4 + b: the up projection's
         const int g = 4 * k + (lane & 3);
-        if (lane < 8 && g < G) raw.b[0] = __ldg(p.sB + (tl.col0 + (lane >> 2) * p.N) / 128 * G + g);
+        if (lane < 8 && g < G) raw.v[0] = __ldg(p.sB + (tl.col0 + (lane >> 2) * p.N) / 128 * G + g);
       } else {
         const int64_t nb = tl.col0 / 128 + (lane >> 2);
         const int g = 4 * k + (lane & 3);
         if (lane < 12 && g < G && nb * 128 < p.N)
-          raw.b[0] = __ldg(p.sB + (static_cast<int64_t>(tl.expert) * (p.N / 128) + nb) * G + g);
+          raw.v[0] = __ldg(p.sB + (static_cast<int64_t>(tl.expert) * (p.N / 128) + nb) * G + g);
       }
     };
     // Packs the slot into its shared-memory blocks once the MMA thread has copied the
     // ring slot's previous contents.  Returns false (warp-uniform) on abort or timeout.
     auto emit = [&](int i, int64_t sc, const Raw& raw) -> bool {
       const Tile tl = tile_of(i);
-      uint32_t wa[4], wb[8];
+      uint32_t wb[8];                                    // A: the first four
+      if (of_a) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        wa[j] = 0;
+        for (int j = 0; j < 4; ++j) {
+          wb[j] = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) wa[j] |= ue8m0_of(raw.a[4 * j + b], bad) << (8 * b);
-      }
-      if (ROW_B) {
+          for (int b = 0; b < 4; ++b) wb[j] |= ue8m0_of(raw.v[4 * j + b], bad) << (8 * b);
+        }
+      } else if (ROW_B) {
 #pragma unroll
         for (int j = 0; j < 7; ++j) {
           wb[j] = 0;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) wb[j] |= ue8m0_of(raw.b[4 * j + b], bad) << (8 * b);
+          for (int b = 0; b < 4; ++b) wb[j] |= ue8m0_of(raw.v[4 * j + b], bad) << (8 * b);
         }
       } else if (GATED) {
-        const uint32_t byte = ue8m0_of(raw.b[0], bad);
+        const uint32_t byte = ue8m0_of(raw.v[0], bad);
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int b = 0; b < 8; ++b) w[b >> 2] |= __shfl_sync(0xFFFFFFFFu, byte, b) << (8 * (b & 3));
 #pragma unroll
         for (int j = 0; j < 8; ++j) wb[j] = w[j >> 2];
       } else {
-        const uint32_t byte = ue8m0_of(raw.b[0], bad);
+        const uint32_t byte = ue8m0_of(raw.v[0], bad);
         uint32_t w[3];
 #pragma unroll
         for (int jb = 0; jb < 3; ++jb) {
@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(Ue8m0Cfg<GROUPED, GATED>::kThreads, 1)
                                  abort_flag);
       if (!__all_sync(0xFFFFFFFFu, got)) return false;
       uint8_t* blk = smem + Cfg::sf + r * Cfg::kSfBytes;
-      *reinterpret_cast<uint4*>(blk + 16 * lane) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-      *reinterpret_cast<uint4*>(blk + Cfg::kSfA + 16 * lane) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
-      *reinterpret_cast<uint4*>(blk + 2 * Cfg::kSfA + 16 * lane) = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+      *reinterpret_cast<uint4*>(blk + (of_a ? 0 : Cfg::kSfA) + 16 * lane) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+      if (!of_a)
+        *reinterpret_cast<uint4*>(blk + 2 * Cfg::kSfA + 16 * lane) = make_uint4(wb[4], wb[5], wb[6], wb[7]);
       fence_proxy_async_smem();                          // visible to tcgen05.cp
       __syncwarp();
       if (lane == 0) mbar_arrive(sfull_bar(r));
