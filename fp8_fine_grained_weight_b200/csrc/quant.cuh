@@ -509,8 +509,12 @@ __global__ void __launch_bounds__(256, 6) quant_act_dual_kernel(const __grid_con
 // symmetric under transposition (a block's amax is that of its transpose), so these are
 // exactly the codes and scales of the transposed bf16 matrix: the operand a Dgrad GEMM
 // (dX = dY W) needs, without requantizing from bf16.  Grid (K/128, N/128), 256 threads,
-// one block per CTA through shared memory (row pitch 132 bytes).
-constexpr int kTrPitch = 132;
+// one block per CTA through shared memory.  Bound by HBM: a thread reads 16 rows of four bytes
+// as words, transposes 4 x 4 bytes at a time in registers and writes four rows of 16 bytes.
+// Sixteen rows take 16 bytes more than their data, so that the eight lanes of an output row
+// read distinct banks.  Measured (4096 x 7168): 11.6 us in the gated layer's step, 22.4 us when each
+// byte was read from shared memory by itself.
+__device__ __forceinline__ uint32_t tr_offset(int r) { return 128u * r + 16u * (r / 16); }
 
 __global__ void __launch_bounds__(256) transpose_blocks_kernel(const uint8_t* __restrict__ q,
                                                                const float* __restrict__ s,
@@ -518,33 +522,36 @@ __global__ void __launch_bounds__(256) transpose_blocks_kernel(const uint8_t* __
                                                                uint8_t* __restrict__ qt,
                                                                float* __restrict__ st,
                                                                int64_t ldqt, int NB) {
-  __shared__ __align__(16) uint8_t blk[128 * kTrPitch];
+  __shared__ __align__(16) uint8_t blk[128 * 128 + 8 * 16];
   const int64_t g = blockIdx.x, nb = blockIdx.y;
   const uint8_t* src = q + nb * 128 * ldq + g * 128;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {                     // 128 rows x 128 B, 16 B per thread
     const int idx = j * 256 + threadIdx.x;
     const int r = idx >> 3, chunk = idx & 7;
-    const uint4 v = *reinterpret_cast<const uint4*>(src + r * ldq + chunk * 16);
-    uint32_t* d = reinterpret_cast<uint32_t*>(blk + r * kTrPitch + chunk * 16);
-    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    *reinterpret_cast<uint4*>(blk + tr_offset(r) + chunk * 16) =
+        *reinterpret_cast<const uint4*>(src + r * ldq + chunk * 16);
   }
   __syncthreads();
-  uint8_t* dst = qt + g * 128 * ldqt + nb * 128;
+  // input rows 16 chunk .. + 15, columns c .. c + 3
+  const int chunk = threadIdx.x & 7, c = 4 * (threadIdx.x >> 3);
+  uint32_t o[4][4];                                 // [output row][four bytes]
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {                     // output row c = input column c
-    const int idx = j * 256 + threadIdx.x;
-    const int c = idx >> 3, chunk = idx & 7;
+  for (int b = 0; b < 4; ++b) {
     uint32_t w[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int r = chunk * 16 + 4 * b;
-      w[b] = static_cast<uint32_t>(blk[r * kTrPitch + c]) | (static_cast<uint32_t>(blk[(r + 1) * kTrPitch + c]) << 8) |
-             (static_cast<uint32_t>(blk[(r + 2) * kTrPitch + c]) << 16) |
-             (static_cast<uint32_t>(blk[(r + 3) * kTrPitch + c]) << 24);
-    }
-    *reinterpret_cast<uint4*>(dst + c * ldqt + chunk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i)
+      w[i] = *reinterpret_cast<const uint32_t*>(blk + tr_offset(16 * chunk + 4 * b + i) + c);
+    const uint32_t t0 = __byte_perm(w[0], w[1], 0x5140), t1 = __byte_perm(w[2], w[3], 0x5140);   // columns 0, 1
+    const uint32_t t2 = __byte_perm(w[0], w[1], 0x7362), t3 = __byte_perm(w[2], w[3], 0x7362);   // 2, 3
+    o[0][b] = __byte_perm(t0, t1, 0x5410);
+    o[1][b] = __byte_perm(t0, t1, 0x7632);
+    o[2][b] = __byte_perm(t2, t3, 0x5410);
+    o[3][b] = __byte_perm(t2, t3, 0x7632);
   }
+  uint8_t* dst = qt + (g * 128 + c) * ldqt + nb * 128 + 16 * chunk;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + i * ldqt) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
   if (threadIdx.x == 0) st[g * NB + nb] = s[nb * G + g];
 }
 
