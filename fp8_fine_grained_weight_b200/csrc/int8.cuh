@@ -201,8 +201,9 @@ __global__ void __launch_bounds__(kInt8Threads)
 // most 64 bytes a cycle from L2; a 128 x 256 tile alone needs 48 KB per 512-cycle stage, half
 // as much again, a paired one 32 KB.
 //
-// Measured: 4096 x 7168 x 7168 in 135 us on pairs (0.94 of twice the bf16 peak) and 144 us on
-// single CTAs; gated 4096 x 2048 x 7168 in 80 and 88 us.
+// Measured: 4096 x 7168 x 7168 in 122-132 us on pairs (0.96-1.03 of twice the bf16 peak, 88 % of
+// the tensor pipe's cycles) and 141 us on single CTAs; gated 4096 x 2048 x 7168 in 76-79 us on
+// pairs.  With the MMAs issued from a lane's own registers, not uniform ones: 135, 144 and 80.
 struct Int8Args {
   const float* sA;      // [M]
   const float* sB;      // [N], gated [2N]

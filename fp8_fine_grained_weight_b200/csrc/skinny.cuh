@@ -17,12 +17,12 @@
 //               FP8: a fresh accumulator (of four) per group, promoted by the epilogue.
 //   warp 2      FP8: scale producer, MP row scales and the two weight scales per group
 //               INT8: puts the tile's row and weight scales into shared memory
-//   warp 3      idle
+//   warp 3      idle; FP8 whose scales shall be powers of two: checks them
 //   warps 4-7   epilogue: thread t owns weight row t of the tile.  FP8: per group
 //               acc[m] += (P sW) sA[m] in FP32 registers.
-// Measured: INT8 1 x 7168 x 2048 in 7.0 us, 64 x 7168 x 7168 in 14.2 us (8 us of streaming at the
-// HBM rate, 2 of launch, the rest joining the sums); FP8 gated 16 x 2048 x 7168 in 10.7 us.  The
-// wide kernels take 9-10, 24 and 34 us.
+// Measured: INT8 1 x 7168 x 2048 in 7.1 us, 64 x 7168 x 7168 in 13.8 us (8 us of streaming at the
+// HBM rate, 2 of launch, the rest joining the sums); FP8 gated 16 x 2048 x 7168 in 10.0 us (the
+// wide kernel: 31).  Against the wide kernels at more rows: beside the rule that chooses.
 //
 // All eight warps then sum the slices.  Two CTAs fit on an SM (about 100 KB, 128 registers).
 //
