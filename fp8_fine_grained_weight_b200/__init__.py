@@ -654,7 +654,8 @@ def gemm_blockscaled_gated(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor,
 def gemm_gated_ue8m0(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
                      with_gu: bool = False, out=None):
     """gemm_blockscaled_gated for power-of-two scales, applied inside the tensor core: the faster of
-    the two.  Scales that are not powers of two are reported through ``device_error``."""
+    the two.  Scales that are not powers of two in [2^-127, 2^127] are reported through
+    ``device_error``."""
     return _gemm_gated("fp8_gemm_gated_ue8m0", qa, sa, qw, sw, with_gu, out)
 
 

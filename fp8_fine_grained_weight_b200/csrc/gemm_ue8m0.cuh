@@ -15,7 +15,7 @@
 // inside the same acceptance band against the oracle).  Scales that are not powers of
 // two in [2^-127, 2^127] cannot be expressed in UE8M0: the kernel records
 // (kSiteScaleFormat << 8) | FP8Q_ERR_SCALE in the device error word for them and goes on
-// with scale 1.
+// with scale 1 (2^-127 for smaller powers of two).
 //
 // GATED: the gated feed-forward projections, h = silu(g) u with g and u the products with the
 // gate's N rows of B and the N rows after them (B is [2N, K]); p.gu takes g and u in bf16 when
@@ -130,7 +130,8 @@ __device__ __forceinline__ uint32_t ue8m0_of(float s, bool& bad) {
   if ((b & 0x7FFFFFu) == 0 && e >= 1 && e <= 254) return e;
   if (b == 0x00400000u) return 0;                 // 2^-127, the smallest UE8M0 value
   bad = true;
-  return 127;
+  // a smaller power of two (a tile below 2.7e-36): 2^-127, so that the tile stays negligible
+  return b - 1u < 0x003FFFFFu && (b & (b - 1u)) == 0 ? 0 : 127;
 }
 
 template <bool ROW_B, bool OUT_BF16, bool GROUPED, bool GATED = false>

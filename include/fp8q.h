@@ -193,8 +193,8 @@ int fp8_gemm_blockscaled_quant(const uint8_t* A, const float* sA, int64_t ld_sa,
  * differs).  Every scale the call reads must be a power of two in [2^-127, 2^127]; any
  * other value (not a power of two, zero, negative, inf, nan) is not detectable on the
  * host: the kernel records (8 << 8) | FP8Q_ERR_SCALE in the device error word, uses 1 in
- * its place and finishes the call (C is then not the product).  Tiles of 128 x 224; no
- * workspace.
+ * its place (2^-127 for a smaller power of two) and finishes the call (C is then not the
+ * product).  Tiles of 128 x 224; no workspace.
  */
 int fp8_gemm_blockscaled_ue8m0(const uint8_t* A, const float* sA, int64_t ld_sa,
                                const uint8_t* B, const float* sB, int64_t ld_sb, int b_scale_mode,
@@ -363,7 +363,7 @@ int fp8_gemm_blockscaled_gated(const uint8_t* A, const float* sA, int64_t ld_sa,
 /*
  * fp8_gemm_blockscaled_gated for power-of-two scales [P2], applied inside the tensor core as by
  * fp8_gemm_blockscaled_ue8m0 (with few rows as by fp8_gemm_blockscaled_gated).  Scales that are
- * not powers of two are reported in the device error word, as there.
+ * not powers of two in [2^-127, 2^127] are reported in the device error word, as there.
  */
 int fp8_gemm_gated_ue8m0(const uint8_t* A, const float* sA, int64_t ld_sa, const uint8_t* W,
                          const float* sW, void* H, int64_t ldh, void* GU, int64_t ldgu, int64_t M,
@@ -411,6 +411,10 @@ int fp8q_quant_act_dual_padded(const void* x_bf16, int64_t M, int64_t K, int64_t
  * backward  fp8q_gated_backward_quant, then dX = D W (K = 2N) unless dX is NULL, and
  *           dW = D^T X (K = T rounded up to 128) unless dW is NULL, by the block-scaled GEMMs
  *           (power-of-two scales: fp8_gemm_blockscaled_ue8m0)
+ *
+ * With power-of-two scales a tile whose largest magnitude is above 0 and at most
+ * 448 * 2^-128 (1.3e-36) has a scale below 2^-127: it is reported as there, and its values
+ * are taken as if its scale were 2^-127.
  * Any T; N and K multiples of 128; every pointer on 16 bytes.  T == 0: forward quantizes W only,
  * backward does nothing (dW is not written).
  */

@@ -187,6 +187,23 @@ def test_forward_of_powers_of_two_reports_other_scales(fq):
         assert fq.device_error() == 0
 
 
+def test_forward_of_powers_of_two_below_the_smallest_scale(fq):
+    """A tile whose scale is a power of two under 2^-127 is reported and counts with 2^-127: g and u
+    are off by at most 448 2^-127 sum |w| for it, the other rows' by nothing."""
+    import torch
+    M, N, K = 300, 256, 512
+    _, _, (qa, sa), (qw, sw) = operands(M, N, K, True, 6)
+    sa[2, 7], sa[0, 299] = 2.0 ** -130, 2.0 ** -149
+    C, T = oracle.gemm_blockscaled_ref(qa, sa, qw, sw)
+    h, gu = fq.gemm_gated_ue8m0(*[to_dev(t) for t in (qa, sa, qw, sw)], with_gu=True)
+    assert fq.device_error() == (8 << 8) | 7
+    wmax = 448 * float(sw.max())
+    C = C.astype(np.float64)
+    tol = 2e-5 * T * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(C) + 128 * 448 * 2.0 ** -127 * wmax + 1e-30
+    assert (np.abs(host(gu).astype(np.float64) - C) <= tol).all()
+    check_h(host(h), C, T)
+
+
 # -------------------------------------------------------------------------------- backward
 
 def grads64(dh, gu):
