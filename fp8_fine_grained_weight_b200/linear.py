@@ -39,8 +39,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (_call, _launch, _require_cuda, _same_device, gemm_blockscaled, gemm_blockscaled_gated,
-               gemm_blockscaled_ue8m0, quant_act_1x128, quant_act_dual, quant_weight_128x128,
-               transpose_blocks)
+               gemm_blockscaled_ue8m0, gemm_gated_ue8m0, quant_act_1x128, quant_act_dual,
+               quant_weight_128x128, transpose_blocks)
 
 
 def _gemm(pow2: bool):
@@ -171,7 +171,7 @@ def fp8_gated_linear(x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> to
         return FP8GatedLinearFunction.apply(x, w, pow2)
     qx, sx = quant_act_1x128(_packed(x), pow2)
     qw, sw = quant_weight_128x128(_packed(w), pow2)
-    return gemm_blockscaled_gated(qx, sx, qw, sw)
+    return (gemm_gated_ue8m0 if pow2 else gemm_blockscaled_gated)(qx, sx, qw, sw)    # as with gradients
 
 
 class FP8GatedLinear(torch.nn.Module):

@@ -1,0 +1,40 @@
+"""The gated layer's paths on the CPU: which library calls each makes and with which arguments (the
+calls recorded instead of made)."""
+import pytest
+import torch
+
+import fp8_fine_grained_weight_b200 as fq
+import fp8_fine_grained_weight_b200.linear as linear
+from fp8_fine_grained_weight_b200.linear import fp8_gated_linear
+
+bf16 = torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    log = []
+    for module in (fq, linear):
+        monkeypatch.setattr(module, "_require_cuda", lambda t, name: None)
+        monkeypatch.setattr(module, "_call", lambda name, *args: log.append((name, args)))
+    monkeypatch.setattr(fq, "_stream", lambda t: 0)
+    monkeypatch.setattr(linear, "_gated_bytes", lambda *a: (256, 256, 256))
+    return log
+
+
+def names(calls):
+    return [name for name, _ in calls]
+
+
+@pytest.mark.parametrize("pow2,product", [(False, "fp8_gemm_blockscaled_gated"), (True, "fp8_gemm_gated_ue8m0")])
+def test_without_gradients_the_scales_choose_the_product(calls, pow2, product):
+    """The product that the layer runs with gradients: FP32 scales promoted, powers of two applied by the
+    tensor core."""
+    x, w = torch.empty(4, 128, dtype=bf16), torch.empty(256, 128, dtype=bf16)
+    assert fp8_gated_linear(x, w, pow2).shape == (4, 128)
+    assert names(calls) == ["fp8q_quant_act_1x128", "fp8q_quant_weight_128x128", product]
+    assert all(args[-2] == int(pow2) for _, args in calls[:2])
+    calls.clear()
+    w.requires_grad_(True)
+    with torch.no_grad():
+        fp8_gated_linear(x, w, pow2)
+    assert names(calls)[-1] == product
