@@ -36,6 +36,7 @@ from typing import Optional
 
 import torch
 
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (_call, _launch, _require_cuda, _same_device, gemm_blockscaled, gemm_blockscaled_gated,
@@ -131,6 +132,8 @@ class FP8GatedLinearFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dh: torch.Tensor):
+        if forward_ad.unpack_dual(dh).tangent is not None:
+            raise NotImplementedError("fp8_gated_linear has no forward-mode derivative")
         kept, = ctx.saved_tensors
         T, N, K, kept_for_dw, pow2 = ctx.sizes
         for_dx, for_dw, _ = ctx.needs_input_grad
@@ -152,7 +155,7 @@ def fp8_gated_linear(x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> to
     """H = silu(X Wg^T) * (X Wu^T) in FP8, W = [Wg; Wu] stacked (see the module docstring).
 
     x bf16 [T, K], w bf16 [2N, K] -> bf16 [T, N].  Without gradients g and u are not kept.
-    Differentiable once.  When a backward pass is captured into a CUDA graph, no other autograd
+    Differentiable once, in reverse mode; a forward-mode tangent is refused.  When a backward pass is captured into a CUDA graph, no other autograd
     graph of the same leaves may be alive: autograd would run its gradient accumulators on the
     stream of that graph, outside the capture (true of every differentiable function).
     """
@@ -167,7 +170,9 @@ def fp8_gated_linear(x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> to
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     _same_device(w, x.device, "w")
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+    # (the function also refuses a tangent, which the calls below would drop)
+    if (torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)
+            or any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w))):
         return FP8GatedLinearFunction.apply(x, w, pow2)
     qx, sx = quant_act_1x128(_packed(x), pow2)
     qw, sw = quant_weight_128x128(_packed(w), pow2)

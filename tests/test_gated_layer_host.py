@@ -38,3 +38,31 @@ def test_without_gradients_the_scales_choose_the_product(calls, pow2, product):
     with torch.no_grad():
         fp8_gated_linear(x, w, pow2)
     assert names(calls)[-1] == product
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("dual", ["x", "w"])
+@pytest.mark.parametrize("grad_mode", [True, False])
+def test_forward_mode_derivatives_are_refused(calls, pow2, dual, grad_mode):
+    """An operand with a tangent does not require a gradient; its derivative must not come out as zero."""
+    from torch.autograd import forward_ad
+    ops = {"x": torch.zeros(4, 128, dtype=bf16), "w": torch.zeros(256, 128, dtype=bf16)}
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad_mode):
+        fp8_gated_linear(**ops, pow2=pow2)                       # no tangent: taken
+        ops[dual] = forward_ad.make_dual(ops[dual], torch.ones_like(ops[dual]))
+        with pytest.raises(NotImplementedError, match="jvp"):
+            fp8_gated_linear(**ops, pow2=pow2)
+    with pytest.raises((NotImplementedError, RuntimeError)):
+        torch.func.jvp(lambda x: fp8_gated_linear(x, ops["w"], pow2), (torch.zeros(4, 128, dtype=bf16),),
+                       (torch.ones(4, 128, dtype=bf16),))
+
+
+def test_a_tangent_of_the_upstream_gradient_is_refused(calls):
+    from torch.autograd import forward_ad
+    x = torch.zeros(4, 128, dtype=bf16, requires_grad=True)
+    h = fp8_gated_linear(x, torch.zeros(256, 128, dtype=bf16))
+    dh = torch.zeros(4, 128, dtype=bf16)
+    with forward_ad.dual_level():
+        torch.autograd.grad(h, x, dh, retain_graph=True)         # no tangent: taken
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            torch.autograd.grad(h, x, forward_ad.make_dual(dh, torch.ones_like(dh)))
