@@ -181,6 +181,17 @@ def _dense(t: torch.Tensor, dtype, name: str, shape, device: torch.device) -> No
                          f"got {tuple(t.shape)} with strides {t.stride()}")
 
 
+def _ceil_to(n: int, multiple: int) -> int:
+    return -(-n // multiple) * multiple
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Row stride of a 2-D operand.  A single row's stride says nothing (a transposed column may
+    carry any): there, its columns rounded up to 16, which meets every alignment rule."""
+    rows, cols = t.shape
+    return t.stride(0) if rows != 1 else _ceil_to(cols, 16)
+
+
 # --------------------------------------------------------------------------------------
 # quantization
 # --------------------------------------------------------------------------------------
@@ -198,12 +209,12 @@ def quant_act_1x128(x: torch.Tensor, pow2: bool = False, ld_scale: Optional[int]
         q, s = out
         _rows(_u8(q), torch.uint8, "q", M, K, x.device)
         _rows(s, torch.float32, "s", K // 128, M, x.device)
-        ld = s.stride(0)
+        ld = s.stride(0) if s.shape[0] != 1 else max(s.stride(0), s.shape[1])    # of one group it says nothing
         if ld_scale is not None and int(ld_scale) != ld:
             raise ValueError(f"ld_scale {ld_scale} disagrees with the row stride {ld} of s")
     with _on(x):
-        _call("fp8q_quant_act_1x128", x.data_ptr(), M, K, x.stride(0), _u8(q).data_ptr(),
-              _u8(q).stride(0), s.data_ptr(), ld, int(bool(pow2)), _stream(x))
+        _call("fp8q_quant_act_1x128", x.data_ptr(), M, K, _pitch(x), _u8(q).data_ptr(),
+              _pitch(_u8(q)), s.data_ptr(), ld, int(bool(pow2)), _stream(x))
     return q, s
 
 
@@ -284,7 +295,7 @@ def quant_rowwise(x: torch.Tensor, pow2: bool = False):
     q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     s = torch.empty((M,), dtype=torch.float32, device=x.device)
     with _on(x):
-        _call("fp8q_quant_rowwise", x.data_ptr(), M, K, x.stride(0), q.data_ptr(), q.stride(0),
+        _call("fp8q_quant_rowwise", x.data_ptr(), M, K, _pitch(x), q.data_ptr(), q.stride(0),
               s.data_ptr(), int(bool(pow2)), _stream(x))
     return q, s
 
@@ -521,20 +532,9 @@ def gemm_nopromo(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch
 # 8-bit feed-forward: INT8 products and the gated projections
 # --------------------------------------------------------------------------------------
 
-def _ceil_to(n: int, multiple: int) -> int:
-    return -(-n // multiple) * multiple
-
-
 def _new(rows: int, cols: int, dtype, device, pitch: Optional[int] = None) -> torch.Tensor:
     """An uninitialized [rows, cols] tensor (empty_strided costs 0.8 us less than empty)."""
     return torch.empty_strided((rows, cols), (cols if pitch is None else pitch, 1), dtype=dtype, device=device)
-
-
-def _pitch(t: torch.Tensor) -> int:
-    """Row stride of a 2-D operand.  A single row's stride says nothing (a transposed column may
-    carry any): there, its columns rounded up to 16, which meets every alignment rule."""
-    rows, cols = t.shape
-    return t.stride(0) if rows != 1 else _ceil_to(cols, 16)
 
 
 def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):

@@ -66,3 +66,33 @@ def test_a_tangent_of_the_upstream_gradient_is_refused(calls):
         torch.autograd.grad(h, x, dh, retain_graph=True)         # no tangent: taken
         with pytest.raises(NotImplementedError, match="forward-mode"):
             torch.autograd.grad(h, x, forward_ad.make_dual(dh, torch.ones_like(dh)))
+
+
+def test_a_single_token_of_any_row_stride(calls):
+    """A row taken out of a transposed or oddly pitched buffer stays contiguous to torch whatever its row
+    stride says; the quantizers that the layer runs get a stride that the library takes."""
+    w = torch.zeros(256, 128, dtype=bf16)
+    for x in (torch.zeros(128, 1, dtype=bf16).t(), torch.zeros(3, 131, dtype=bf16)[1:2, 3:]):
+        assert x.shape == (1, 128) and x.is_contiguous() and x.stride(0) != 128
+        fp8_gated_linear(x, w)
+        args = dict(calls)["fp8q_quant_act_1x128"]
+        assert args[1:4] == (1, 128, 128) and args[5] == 128
+        fq.quant_rowwise(x)
+        assert calls[-1][1][1:4] == (1, 128, 128)
+        calls.clear()
+
+
+def test_quantizers_take_single_rows_of_outputs(calls):
+    """Outputs with one row, or scales of one group, whose row stride is not the pitch."""
+    u8, f32 = torch.uint8, torch.float32
+    q, s = torch.zeros(256, 1, dtype=u8).t(), torch.zeros(2, 9, dtype=f32)
+    fq.quant_act_1x128(torch.zeros(1, 256, dtype=bf16), out=(q, s))
+    assert calls[-1][1][5] == 256 and calls[-1][1][7] == 9
+    one_group = torch.zeros(5, 1, dtype=f32).t()                 # [1, 5], row stride 1
+    fq.quant_act_1x128(torch.zeros(5, 128, dtype=bf16), out=(torch.zeros(5, 128, dtype=u8), one_group))
+    assert calls[-1][1][7] >= 5
+    padded = torch.zeros(1, 16, dtype=f32)                       # what ran before: its stride is the pitch
+    fq.quant_act_1x128(torch.zeros(5, 128, dtype=bf16), out=(torch.zeros(5, 128, dtype=u8), padded), ld_scale=16)
+    assert calls[-1][1][7] == 16
+    with pytest.raises(ValueError, match="ld_scale"):
+        fq.quant_act_1x128(torch.zeros(5, 128, dtype=bf16), out=(torch.zeros(5, 128, dtype=u8), padded), ld_scale=8)
