@@ -57,3 +57,15 @@ def assert_gemm_close(name, C: np.ndarray, C_ref: np.ndarray, T: np.ndarray, bf1
 def rel_err_stats(C, C_ref, T):
     e = np.abs(np.asarray(C, np.float64) - C_ref) / np.maximum(T, 1e-300)
     return float(e.max()), float(np.median(e))
+
+
+def assert_within(name, got, ref, tol):
+    """|got - ref| <= tol everywhere.  A NaN on either side fails, as it compares false."""
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    with np.errstate(invalid="ignore"):
+        ok = np.abs(got - ref) <= tol
+    if not ok.all():
+        bad = np.argwhere(~ok)
+        first = [(tuple(int(i) for i in b), float(got[tuple(b)]), float(ref[tuple(b)])) for b in bad[:4]]
+        raise AssertionError(f"{name}: {len(bad)} of {got.size} outside the tolerance; first (idx, got, ref) {first}")
