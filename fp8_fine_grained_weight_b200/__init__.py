@@ -542,7 +542,8 @@ def quant_int8_rowwise(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.
 
     Per token for activations, per output channel for weights.  Any K; the codes' rows are
     allocated 16 bytes apart or a multiple (q is strided when K % 16 != 0), as the products
-    need them.  A row that holds Inf or NaN gets the scale NaN.
+    need them.  A row that holds Inf or NaN gets the scale NaN and codes 0; a row whose largest
+    magnitude is below 2^-100 counts as zeros (scale 1, codes 0).
     """
     _need(x, torch.bfloat16, "x", 2)
     M, K = x.shape

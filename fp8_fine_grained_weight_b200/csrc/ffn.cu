@@ -146,6 +146,10 @@ int sm_count() {
 //   INT8 N 2048 K 1496        128 rows 6.7 / 7.1, 256 8.0 / 7.3;   N 512 K 7168, 512 rows 10.1 / 15.1
 //   INT8 gated N 2048 K 7168  128 rows 12.4 / 15.7, 256 15.6 / 15.8, 384 17.7 / 16.7
 //   FP8 gated N 2048 K 7168   64 rows 11.5 / 30.8, 256 22.2 / 31.4, 384 37.2 / 31.5
+// and against the wide kernel for power-of-two scales:
+//   N 2048 K 7168             64 rows 12.0 / 25.7, 256 22.1 / 26.2;   N 4096, 128 rows 22.4 / 26.9
+//   N 1024 K 2048             64 rows 6.5 / 10.0, 256 9.0 / 10.3, 512 11.1 / 10.6
+//   N 512 K 7168              256 rows 10.6 / 23.0, 512 15.0 / 24.6
 bool few_rows(int64_t M, int64_t rows, int64_t G, int sms, bool fp8) {
   if (M <= 64) return true;
   if (M > 512) return false;

@@ -35,11 +35,12 @@ namespace fp8q {
 //   warp 2      scale producer (slots of four groups: 128 row scales, a gate and an up scale)
 //   warps 4-11  promotion and epilogue.  Registers: 128 threads * 40 + 256 * 232 <= 384 * 168.
 //
-// Measured: 223-228 us at 8192 x 2048 x 7168 (0.63-0.65 of the FP8 peak), 38 us at 1000 rows; for
-// power-of-two scales the tensor core applies them in 178 and 29 us (gemm_ue8m0.cuh).  The
-// promotion loop bounds it (tensor pipe about half busy): about 900 cycles per group against 512 of MMAs, of
-// which the 64 packed FMAs per thread are 260.  Three warpgroups on 96 columns (277 us) and four
-// at 112 registers (250 us) measured slower; one issuer and per-thread arrivals 233 us.
+// Measured: 223-251 us at 8192 x 2048 x 7168 over the machines seen (0.57-0.65 of the FP8 peak), 38-42
+// us at 1000 rows; for power-of-two scales the tensor core applies them in 178-184 and 29 us
+// (gemm_ue8m0.cuh).  The promotion loop bounds it (tensor pipe about half busy): about 900 cycles per
+// group against 512 of MMAs, of which the 64 packed FMAs per thread are 260.  Three warpgroups on 96
+// columns (277 us) and four at 112 registers (250 us) measured slower; one issuer and per-thread
+// arrivals 233 us.
 struct GatedArgs {
   const float* sA;      // group-major [G][ld_sa]
   int64_t ld_sa;

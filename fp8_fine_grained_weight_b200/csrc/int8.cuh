@@ -14,7 +14,8 @@ namespace fp8q {
 // ---------------------------------------------------------------- per-row quantization
 //
 //   a = max_k |x[m, k]|
-//   a < 2^-100:      s = 1, q = 0          (a zero row; below it 127 / a leaves FP32's range)
+//   a < 2^-100:      s = 1, q = 0          (counts as a zero row: a chosen threshold, above the 2^-121
+//                                          below which 127 / a would leave FP32's range)
 //   a Inf or NaN:    s = NaN, q = 0        (every product with the row is then NaN)
 //   otherwise        s = RN_f32(a / 127), r = RN_f32(127 / a), q = round-half-even(x r)
 //
@@ -123,7 +124,9 @@ __global__ void __launch_bounds__(kInt8Threads)
 // first and last 16-byte boundary are read whole (the elements before and after them one by
 // one), and put into shared memory, from where each thread takes four elements at a time
 // in the order of the codes.  Rows longer than the buffer are read element by element,
-// twice.
+// twice.  Bound by the block per row, whatever its length, with its barrier and 33 KB of shared
+// memory: 16384 rows of 100 elements 28 us (of 104, which take the kernel above: 5.0), of 1001 36 us (1000:
+// 8.1), of 2047 43 us; 4096 rows of 7167 22 us (0.61 of HBM).
 constexpr int kInt8Staged = 16384;    // elements
 
 __global__ void __launch_bounds__(kInt8Threads)

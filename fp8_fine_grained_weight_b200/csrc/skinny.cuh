@@ -4,8 +4,8 @@
 // With few rows of A the weight's bytes bound the product, and a grid of 128-row tiles of A
 // would use a few SMs only.  So the operands change places: the tensor core's 128 rows are
 // rows of the weight, its MP columns are rows of A (MP = 16 .. 128, rows past M read as
-// zeros), and K is split over the CTAs of a cluster, so that about twice as many CTAs as SMs
-// stream the weight.  Their partial sums meet in shared memory: each CTA leaves its
+// zeros), and K is split over the CTAs of a cluster of at most four, so that up to two CTAs per SM
+// stream the weight (a gated product of N = 2048 has 32 tiles: 128 CTAs in all).  Their partial sums meet in shared memory: each CTA leaves its
 // [MP][128] partials in its own, the cluster synchronizes, and each CTA sums a slice of the outputs
 // over the cluster in CTA order (a fixed order; INT32 sums are exact in any) and finishes it:
 // one launch, no workspace, no atomics.

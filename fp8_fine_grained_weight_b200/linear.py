@@ -154,7 +154,8 @@ class FP8GatedLinearFunction(torch.autograd.Function):
 def fp8_gated_linear(x: torch.Tensor, w: torch.Tensor, pow2: bool = False) -> torch.Tensor:
     """H = silu(X Wg^T) * (X Wu^T) in FP8, W = [Wg; Wu] stacked (see the module docstring).
 
-    x bf16 [T, K], w bf16 [2N, K] -> bf16 [T, N].  Without gradients g and u are not kept.
+    x bf16 [T, K], w bf16 [2N, K] -> bf16 [T, N].  Without gradients the same product runs and g and u are
+    not kept.
     Differentiable once, in reverse mode; a forward-mode tangent is refused.  When a backward pass is captured into a CUDA graph, no other autograd
     graph of the same leaves may be alive: autograd would run its gradient accumulators on the
     stream of that graph, outside the capture (true of every differentiable function).
